@@ -14,8 +14,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoba.so")
-SOURCES = ["moba_api.cu", "meanpool.cu", "gate.cu", "gate_tc.cu", "route.cu", "attn_tc.cu", "merge.cu", "decode.cu", "minmaxpool.cu", "noalloc.cu", "attn_bwd.cu"]
-HEADERS = ["moba_internal.cuh", "ptx.cuh"]
+SOURCES = ["moba_api.cu", "meanpool.cu", "gate.cu", "gate_tc.cu", "route.cu", "attn_tc.cu", "merge.cu", "decode.cu", "minmaxpool.cu", "noalloc.cu", "attn_bwd.cu",
+           "cache_api.cu", "cache_append.cu", "cache_decode.cu", "cache_pages.cu"]
+HEADERS = ["moba_internal.cuh", "cache_internal.cuh", "ptx.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-cudart", "static",

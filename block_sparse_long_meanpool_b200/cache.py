@@ -1,0 +1,227 @@
+"""Paged KV cache in 4 bits: the binding of the moba_cache_* calls (include/moba.h).
+
+A ``KVCache`` holds the keys and values of one attention layer for up to ``num_seqs`` sequences,
+in pages of one block (``chunk_size`` tokens, every KV head) each, as e2m1 codes with an e4m3
+scale per 16 channels.  The calls append to it, attend over it and share, free and pack its
+pages; all of them are queued on the current stream of the cache's device and read lengths,
+tables and page counts there, so a serving loop never waits for the host and can be captured into
+a CUDA graph.  What the device finds wrong (no free page left, an index out of range) is kept in
+the cache's status word until ``cache_status`` reads it.
+
+    c = KVCache(num_pages=2048, num_seqs=64, max_blocks=64, num_kv_heads=8, head_dim=128, chunk_size=512)
+    cache_reserve(c, upto)                        # pages for positions below upto[i]
+    cache_append(c, k, v, cu_new, start)          # prompts, or one token of each sequence
+    out, lse = cache_decode(c, q, topk=3)         # topk=0: full attention
+    cache_fork(c, src, dst); cache_free(c, seqs)  # beams, parallel samples, finished sequences
+    cache_compact(c, smaller)                     # the same sequences in another pool
+"""
+
+import ctypes
+
+import torch
+
+from .moba import MobaCache, MobaError, _check, load_library
+
+GROUP = 16  # channels per scale
+
+_POOLS = ("k_codes", "k_scales", "v_codes", "v_scales")
+
+
+def _fail(msg):
+    raise ValueError(msg)
+
+
+def _need(t, name, shape, dtype, device):
+    """A buffer the kernels read or write whole: exact shape, dtype, layout and device."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _fail(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
+              f"{tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'} on {t.device}")
+
+
+class KVCache:
+    """The buffers of a paged 4-bit cache.
+
+    ``k_codes``, ``v_codes`` uint8 [num_pages, Hkv, chunk, d / 2]; ``k_scales``, ``v_scales``
+    float8_e4m3fn [num_pages, Hkv, chunk, d / 16]; ``k_mean`` fp32 [num_pages, Hkv, d]; ``table``
+    int32 [num_seqs, max_blocks] (-1: no page); ``lengths`` int32 [num_seqs]; ``refs`` int32
+    [num_pages]; ``status`` int32 [1].  A held value is e2m1(code) * e4m3(scale) * 2^exp (``k_exp``
+    or ``v_exp``: 0 serves values up to 2688, and steps as small as 2^-10).  The buffers may be
+    read and their contents replaced, but not the tensors themselves.
+    """
+
+    def __init__(self, num_pages, num_seqs, max_blocks, num_kv_heads, head_dim, chunk_size, device="cuda",
+                 k_exp=0, v_exp=0):
+        if min(num_pages, num_seqs, max_blocks, num_kv_heads, head_dim, chunk_size) < 1:
+            _fail("the sizes of a cache must be >= 1")
+        if head_dim % GROUP:
+            _fail(f"head_dim must be a multiple of {GROUP}")
+        rows = (num_pages, num_kv_heads, chunk_size)
+
+        def empty(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        def ints(shape, value=0):
+            return torch.full(shape, value, dtype=torch.int32, device=device)
+
+        self._bind(empty(rows + (head_dim // 2,), torch.uint8), empty(rows + (head_dim // GROUP,), torch.float8_e4m3fn),
+                   empty(rows + (head_dim // 2,), torch.uint8), empty(rows + (head_dim // GROUP,), torch.float8_e4m3fn),
+                   empty((num_pages, num_kv_heads, head_dim), torch.float32), ints((num_pages,)),
+                   ints((num_seqs, max_blocks), -1), ints((num_seqs,)), ints((1,)), k_exp, v_exp)
+
+    @classmethod
+    def from_tensors(cls, k_codes, k_scales, v_codes, v_scales, k_mean, refs, table, lengths, status=None,
+                     k_exp=0, v_exp=0):
+        """A cache over existing buffers (``status``: made when not given)."""
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=table.device)
+        c = cls.__new__(cls)
+        c._bind(k_codes, k_scales, v_codes, v_scales, k_mean, refs, table, lengths, status, k_exp, v_exp)
+        return c
+
+    def _bind(self, k_codes, k_scales, v_codes, v_scales, k_mean, refs, table, lengths, status, k_exp, v_exp):
+        if k_codes.dim() != 4 or table.dim() != 2:
+            _fail("k_codes must be [num_pages, Hkv, chunk, d / 2] and table [num_seqs, max_blocks]")
+        pages, heads, chunk, half = k_codes.shape
+        seqs, blocks = table.shape
+        dev, d = k_codes.device, 2 * half
+        if dev.type != "cuda":
+            _fail(f"the cache's buffers must be CUDA tensors, got {dev}")
+        _need(k_codes, "k_codes", (pages, heads, chunk, half), torch.uint8, dev)
+        _need(v_codes, "v_codes", (pages, heads, chunk, half), torch.uint8, dev)
+        _need(k_scales, "k_scales", (pages, heads, chunk, d // GROUP), torch.float8_e4m3fn, dev)
+        _need(v_scales, "v_scales", (pages, heads, chunk, d // GROUP), torch.float8_e4m3fn, dev)
+        _need(k_mean, "k_mean", (pages, heads, d), torch.float32, dev)
+        _need(refs, "refs", (pages,), torch.int32, dev)
+        _need(table, "table", (seqs, blocks), torch.int32, dev)
+        _need(lengths, "lengths", (seqs,), torch.int32, dev)
+        _need(status, "status", (1,), torch.int32, dev)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_mean, self.refs, self.table, self.lengths, self.status = k_mean, refs, table, lengths, status
+        self.num_pages, self.num_kv_heads, self.chunk_size, self.head_dim = pages, heads, chunk, d
+        self.num_seqs, self.max_blocks, self.k_exp, self.v_exp = seqs, blocks, int(k_exp), int(v_exp)
+        self.device = dev
+        self._struct = MobaCache(pages, seqs, blocks, heads, d, chunk, self.k_exp, self.v_exp,
+                                 *[t.data_ptr() for t in (k_codes, k_scales, v_codes, v_scales, k_mean, table,
+                                                          lengths, refs, status)])
+        self._ref = ctypes.byref(self._struct)
+        self._sizes = {}  # workspace bytes by the call's sizes
+        self._lib = load_library()
+        self._size("pages", self._lib.moba_cache_workspace_size)
+
+    def _size(self, key, fn, *args):
+        n = self._sizes.get(key)
+        if n is None:
+            n = fn(self._ref, *args)
+            if n == 0:
+                raise _last_error()
+            self._sizes[key] = n
+        return n
+
+
+def _last_error():
+    from .moba import ERR_INVALID_ARG
+    return MobaError(ERR_INVALID_ARG, load_library().moba_last_error().decode())
+
+
+def _call(c, fn, *args):
+    """fn(cache, *args, stream) on the current stream of the cache's device."""
+    index = c.device.index
+    if torch.cuda.current_device() != index:  # the launch takes the current device
+        with torch.cuda.device(index):
+            return _call(c, fn, *args)
+    status = fn(c._ref, *args, torch.cuda.current_stream(index).cuda_stream)
+    if status:
+        _check(status)
+
+
+def _workspace(c, given, need):
+    if given is None:
+        return torch.empty(need, dtype=torch.uint8, device=c.device)
+    if given.device != c.device or not given.is_contiguous():
+        _fail(f"workspace must be a contiguous tensor on {c.device}")
+    return given
+
+
+def _indices(c, t, name):
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.device != c.device or not t.is_contiguous():
+        _fail(f"{name} must be a contiguous int32 tensor [n] on {c.device}")
+    return t.numel()
+
+
+def cache_reserve(c, upto, workspace=None):
+    """Pages for positions below ``upto`` (int32 [num_seqs]) of every sequence
+    (moba_cache_reserve): the lowest free ones, all or none."""
+    _need(upto, "upto", (c.num_seqs,), torch.int32, c.device)
+    ws = _workspace(c, workspace, c._sizes["pages"])
+    _call(c, c._lib.moba_cache_reserve, upto.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def cache_append(c, k, v, cu_new, start, return_held=False):
+    """Writes new keys and values (moba_cache_append): rows cu_new[i] .. cu_new[i + 1] - 1 of k and
+    v, bf16 [n, Hkv, d], to the positions of sequence i from start[i] on (cu_new int32 [num_seqs + 1],
+    start int32 [num_seqs]).  With ``return_held``, returns (k_held, v_held), bf16 like k and v: the
+    values as the cache holds them, for the attention of the prompt itself."""
+    n = k.shape[0]
+    shape = (n, c.num_kv_heads, c.head_dim)
+    _need(k, "k", shape, torch.bfloat16, c.device)
+    _need(v, "v", shape, torch.bfloat16, c.device)
+    _need(cu_new, "cu_new", (c.num_seqs + 1,), torch.int32, c.device)
+    _need(start, "start", (c.num_seqs,), torch.int32, c.device)
+    held = (torch.empty_like(k), torch.empty_like(v)) if return_held else None
+    _call(c, c._lib.moba_cache_append, k.data_ptr(), v.data_ptr(), cu_new.data_ptr(), start.data_ptr(), n,
+          held[0].data_ptr() if held else None, held[1].data_ptr() if held else None)
+    return held
+
+
+def cache_decode(c, q, topk, softmax_scale=None, workspace=None, out=None, lse=None):
+    """Decode step over the cache (moba_cache_decode): one new query per sequence, q bf16
+    [num_seqs, Hq, d], at its last held token.  ``topk`` counts the own block, 0 attends to every
+    block.  Returns (out bf16 [num_seqs, Hq, d], lse fp32 [Hq, num_seqs])."""
+    if q.dim() != 3:
+        _fail(f"q must be [num_seqs, Hq, d], got {tuple(q.shape)}")
+    hq = q.shape[1]
+    shape = (c.num_seqs, hq, c.head_dim)
+    _need(q, "q", shape, torch.bfloat16, c.device)
+    ws = _workspace(c, workspace, c._size((hq, topk), c._lib.moba_cache_decode_workspace_size, hq, topk))
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=c.device)
+    else:
+        _need(out, "out", shape, torch.bfloat16, c.device)
+    if lse is None:
+        lse = torch.empty((hq, c.num_seqs), dtype=torch.float32, device=c.device)
+    else:
+        _need(lse, "lse", (hq, c.num_seqs), torch.float32, c.device)
+    _call(c, c._lib.moba_cache_decode, q.data_ptr(), hq, topk, softmax_scale or 0.0, ws.data_ptr(),
+          ws.numel() * ws.element_size(), out.data_ptr(), lse.data_ptr())
+    return out, lse
+
+
+def cache_fork(c, src, dst, workspace=None):
+    """Slot dst[i] becomes a copy of slot src[i] (moba_cache_fork; int32 [n] each): full pages are
+    shared, the tokens of a partial last page copied to a free one.  All or none."""
+    n = _indices(c, src, "src")
+    if _indices(c, dst, "dst") != n:
+        _fail("src and dst must have the same number of entries")
+    ws = _workspace(c, workspace, c._sizes["pages"])
+    _call(c, c._lib.moba_cache_fork, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(),
+          ws.numel() * ws.element_size())
+
+
+def cache_free(c, seqs):
+    """Empties the slots ``seqs`` (moba_cache_free; int32 [n])."""
+    _call(c, c._lib.moba_cache_free, seqs.data_ptr(), _indices(c, seqs, "seqs"))
+
+
+def cache_compact(c, into, workspace=None):
+    """Packs c's pages in use into the first pages of the cache ``into`` and writes its table, lengths
+    and refs to match (moba_cache_compact).  ``into`` differs from c in num_pages at most."""
+    if into.device != c.device:
+        _fail(f"into must be on {c.device}")
+    ws = _workspace(c, workspace, c._sizes["pages"])
+    _call(c, c._lib.moba_cache_compact, into._ref, ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def cache_status(c):
+    """Raises MobaError when a call on the cache met an error on the device, and clears it (waits for
+    the current stream)."""
+    _call(c, c._lib.moba_cache_status)

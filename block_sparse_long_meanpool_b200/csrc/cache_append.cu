@@ -1,0 +1,269 @@
+// Writing into the paged 4-bit cache (moba_cache_append): microscaled quantisation of new keys
+// and values, and the mean held key of the blocks that they complete.
+//
+// A group of 16 channels x of a token is held as codes c and a scale s (x, s without the cache's
+// power of two):  a = max|x|,  s = e4m3(min(a / 6, 448)),  c = e2m1(x / s), both rounded to
+// nearest with ties to even; the held value is c s.  Six is the largest e2m1 magnitude, so the
+// group's maximum lands on the last step of the grid.  Streaming: 4 bytes are read per key and
+// value channel pair and 1.125 written.
+//   append_kernel        one CTA per (64-position segment of a sequence's new tokens, KV head)
+//   append_means_kernel  one CTA per (completed block, KV head), and one warp per sequence that
+//                        moves its length
+#include "cache_internal.cuh"
+
+namespace moba {
+namespace cache {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSeg = 64;  // positions per segment, aligned within a block (chunk % 128 == 0)
+
+// The idx-th unit of `unit` positions that new tokens touch, over all sequences (whole == false),
+// or the idx-th unit that they complete (whole == true).  Called by one warp; every lane gets the
+// sequence (-1 past the last) and the unit's index within it.
+__device__ __forceinline__ int find_unit(const View& c, const AppendArgs& a, int unit, bool whole,
+                                         int idx, NewTokens& t, int& u) {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int i0 = 0; i0 < c.seqs; i0 += 32) {
+        const int i = i0 + lane;
+        NewTokens m{0, 0, 0};
+        bool bad = false;
+        if (i < c.seqs) m = new_tokens(c, a.cu, a.start, a.total, i, &bad);
+        int n = 0;
+        if (m.n > 0)
+            n = whole ? (m.first + m.n) / unit - m.first / unit
+                      : (m.first + m.n - 1) / unit - m.first / unit + 1;
+        int incl = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        const bool hit = n > 0 && idx >= base + incl - n && idx < base + incl;
+        const unsigned vote = __ballot_sync(0xffffffffu, hit);
+        if (vote) {
+            const int src = __ffs(vote) - 1;
+            u = idx - base - __shfl_sync(0xffffffffu, incl - n, src);
+            t.first = __shfl_sync(0xffffffffu, m.first, src);
+            t.n = __shfl_sync(0xffffffffu, m.n, src);
+            t.row = __shfl_sync(0xffffffffu, m.row, src);
+            u += t.first / unit;
+            return i0 + src;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return -1;
+}
+
+// A page that may be written: in range and held by one sequence only.
+__device__ __forceinline__ bool own_page(const View& c, int page) {
+    return page >= 0 && page < c.pages && __ldg(c.refs + page) == 1;
+}
+
+struct Quantised {
+    uint2 codes;    // 16 codes
+    uint32_t scale;  // e4m3 byte
+};
+
+// Quantises the 16 bf16 channels in w (x = w * 2^-exp, inv_unit = 2^-exp).
+// x / s is formed as x * (1 / s), within 2^-23 of the quotient, and rounded to fp16 before the
+// e2m1 rounding.  That gives exactly e2m1(x / s): a border of the grid is b = B 2^k with an odd
+// B <= 7, so b s has at most 7 significant bits and x has 8; x / s is either b itself, which
+// fp16 (11 bits) restores, or at least 2^-8 of b away from it, which fp16's 2^-12 cannot bridge.
+__device__ __forceinline__ Quantised quantise(const uint32_t (&w)[8], float inv_unit) {
+    uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    const uint32_t top = max(m & 0xffffu, m >> 16);  // largest magnitude's bits; a NaN is above all
+    Quantised r;
+    const float s6 = fminf(__fdiv_rn(__uint_as_float(top << 16) * inv_unit, 6.f), 448.f);
+    uint16_t e;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.f), "f"(s6));
+    const bool nan = top > 0x7f80u;
+    r.scale = nan ? 0x7fu : (uint32_t)(e & 0xffu);
+    const float s = f16x2_to_f32(e4m3x2_to_f16x2(r.scale)).x;
+    const bool zero = !(s > 0.f);
+    const float inv = zero ? 0.f : __frcp_rn(s) * inv_unit;
+    uint32_t out[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t p = w[4 * h + i];
+            const __half2 q = __floats2half2_rn(__uint_as_float(p << 16) * inv,
+                                                __uint_as_float(p & 0xffff0000u) * inv);
+            const float2 f = __half22float2(q);
+            asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+                : "=r"(b[i])
+                : "f"(f.y), "f"(f.x));
+        }
+        out[h] = zero ? 0u : (b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24);
+    }
+    r.codes = make_uint2(out[0], out[1]);
+    return r;
+}
+
+// Held values of 16 codes as fp16 pairs: code * scale has at most 6 significant bits and a
+// magnitude in [2^-10, 2688], exact in fp16.
+__device__ __forceinline__ void held_f16(uint2 codes, uint32_t scale, uint32_t (&h)[8]) {
+    uint32_t s = e4m3x2_to_f16x2(scale | scale << 8);
+    uint32_t lo[4], hi[4];
+    e2m1x8_to_f16x2(codes.x, lo);
+    e2m1x8_to_f16x2(codes.y, hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = hmul2(lo[i], s);
+        h[4 + i] = hmul2(hi[i], s);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+append_kernel(View c, AppendArgs a) {
+    constexpr int kPerTok = D / kGroup;  // groups of a token
+    __shared__ int s_page, s_off, s_cnt, s_row;
+    const int g = blockIdx.y;
+    if (threadIdx.x < 32) {
+        NewTokens t;
+        int u;
+        const int seq = find_unit(c, a, kSeg, false, blockIdx.x, t, u);
+        if (threadIdx.x == 0) {
+            s_cnt = 0;
+            if (seq >= 0) {
+                const int p0 = max(t.first, u * kSeg), p1 = min(t.first + t.n, (u + 1) * kSeg);
+                const int page = __ldg(c.table + (size_t)seq * c.max_blocks + p0 / c.chunk);
+                if (own_page(c, page)) {  // else the sequence's mover reports it
+                    s_page = page;
+                    s_off = p0 % c.chunk;
+                    s_row = t.row + p0 - t.first;
+                    s_cnt = p1 - p0;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const int cnt = s_cnt;
+    if (cnt == 0) return;
+    const size_t crow = code_row(c, s_page, g), srow = scale_row(c, s_page, g);
+    for (int i = threadIdx.x; i < 2 * cnt * kPerTok; i += kThreads) {
+        const bool is_v = i >= cnt * kPerTok;
+        const int e = is_v ? i - cnt * kPerTok : i;
+        const int tok = e / kPerTok, grp = e - tok * kPerTok;
+        const size_t src = ((size_t)(s_row + tok) * c.hkv + g) * D + grp * kGroup;
+        const uint4* x = reinterpret_cast<const uint4*>((is_v ? a.v : a.k) + src);
+        const uint4 x0 = __ldcs(x), x1 = __ldcs(x + 1);
+        const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        const float unit = is_v ? c.v_unit : c.k_unit;
+        const Quantised r = quantise(w, 1.f / unit);  // a power of two
+        const int at = s_off + tok;
+        *reinterpret_cast<uint2*>((is_v ? c.vc : c.kc) + crow + (size_t)at * (D / 2) + grp * 8) = r.codes;
+        ((is_v ? c.vs : c.ks) + srow)[(size_t)at * kPerTok + grp] = (uint8_t)r.scale;
+        if (a.k_held) {
+            uint32_t h[8], o[8];
+            held_f16(r.codes, r.scale, h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 f = f16x2_to_f32(h[j]);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * unit, f.y * unit);
+                o[j] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            uint4* dst = reinterpret_cast<uint4*>((is_v ? a.v_held : a.k_held) + src);
+            __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
+            __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+        }
+    }
+}
+
+// Mean of the held keys of each block that the new tokens complete, from the page itself: 256
+// threads take (row, group) pairs, each adds its rows in ascending order in fp32, and the rows'
+// sums are added in a fixed order, so the mean does not depend on how the block was filled.
+// CTAs behind `blocks` move the lengths.
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+append_means_kernel(View c, AppendArgs a, int blocks) {
+    constexpr int kPerTok = D / kGroup, kRows = kThreads / kPerTok;
+    __shared__ float sums[kRows][D];
+    __shared__ int s_page;
+    const int tid = threadIdx.x, lane = tid & 31, g = blockIdx.y;
+    if (blockIdx.x >= blocks) {
+        const int i = (blockIdx.x - blocks) * (kThreads / 32) + (tid >> 5);
+        if (g || i >= c.seqs) return;
+        bool bad;
+        const NewTokens t = new_tokens(c, a.cu, a.start, a.total, i, &bad);
+        if (bad && lane == 0) report(c, MOBA_ERR_INVALID_ARG);
+        if (t.n == 0) return;
+        bool ok = true;
+        for (int j = t.first / c.chunk + lane; j <= (t.first + t.n - 1) / c.chunk; j += 32)
+            ok = ok && own_page(c, __ldg(c.table + (size_t)i * c.max_blocks + j));
+        ok = __all_sync(0xffffffffu, ok);
+        if (lane == 0) {
+            if (ok) c.lengths[i] = t.first + t.n;
+            else report(c, MOBA_ERR_INVALID_ARG);
+        }
+        return;
+    }
+    if (tid < 32) {
+        NewTokens t;
+        int u;
+        const int seq = find_unit(c, a, c.chunk, true, blockIdx.x, t, u);
+        if (tid == 0) {
+            const int page = seq >= 0 ? __ldg(c.table + (size_t)seq * c.max_blocks + u) : -1;
+            s_page = own_page(c, page) ? page : -1;
+        }
+    }
+    __syncthreads();
+    if (s_page < 0) return;
+    const uint8_t* codes = c.kc + code_row(c, s_page, g);
+    const uint8_t* scales = c.ks + scale_row(c, s_page, g);
+    const int row = tid / kPerTok, grp = tid - row * kPerTok;
+    float acc[kGroup];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) acc[i] = 0.f;
+    for (int r = row; r < c.chunk; r += kRows) {
+        const uint2 w = *reinterpret_cast<const uint2*>(codes + (size_t)r * (D / 2) + grp * 8);
+        uint32_t h[8];
+        held_f16(w, scales[(size_t)r * kPerTok + grp], h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = f16x2_to_f32(h[i]);
+            acc[2 * i] += f.x;
+            acc[2 * i + 1] += f.y;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) sums[row][grp * kGroup + i] = acc[i];
+    __syncthreads();
+    if (tid < D) {
+        float s = 0.f;
+        for (int r = 0; r < kRows; ++r) s += sums[r][tid];
+        c.mean[((size_t)s_page * c.hkv + g) * D + tid] = s * c.k_unit / (float)c.chunk;
+    }
+}
+
+template <int D>
+cudaError_t launch_append_d(const View& c, const AppendArgs& a, cudaStream_t st) {
+    // A sequence with n > 0 new tokens touches at most (n - 1) / kSeg + 2 segments, and no more
+    // segments than tokens; it completes at most n / chunk + 1 blocks, and no more than tokens.
+    const long long n = a.total;
+    const long long segs = min(n, n / kSeg + 2LL * c.seqs);
+    const long long blocks = min(n, n / c.chunk + c.seqs);
+    append_kernel<D><<<dim3((unsigned)segs, c.hkv), kThreads, 0, st>>>(c, a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int movers = (c.seqs + kThreads / 32 - 1) / (kThreads / 32);
+    append_means_kernel<D><<<dim3((unsigned)(blocks + movers), c.hkv), kThreads, 0, st>>>(c, a, (int)blocks);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append(const View& c, const AppendArgs& a, cudaStream_t st) {
+    if (a.total == 0) return cudaSuccess;
+    return c.d == 64 ? launch_append_d<64>(c, a, st) : launch_append_d<128>(c, a, st);
+}
+
+}  // namespace cache
+}  // namespace moba

@@ -1,0 +1,123 @@
+// Internal declarations of the paged 4-bit KV cache (not part of the C ABI).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moba.h"
+
+namespace moba {
+namespace cache {
+
+constexpr int kGroup = 16;  // channels per scale
+
+// A cache as the kernels see it (moba_cache, include/moba.h).
+struct View {
+    int pages, seqs, max_blocks, hkv, d, chunk;
+    float k_unit, v_unit;  // 2^k_exp, 2^v_exp
+    uint8_t *kc, *ks, *vc, *vs;
+    float* mean;
+    int *table, *lengths, *refs, *status;
+};
+
+// The first error stays until the host reads the word.
+__device__ __forceinline__ void report(const View& c, int code) { atomicCAS(c.status, 0, code); }
+
+// Rows of page p, KV head g: [chunk, d / 2] codes, [chunk, d / 16] scales.
+__device__ __forceinline__ size_t code_row(const View& c, int p, int g) {
+    return ((size_t)p * c.hkv + g) * c.chunk * (c.d / 2);
+}
+__device__ __forceinline__ size_t scale_row(const View& c, int p, int g) {
+    return ((size_t)p * c.hkv + g) * c.chunk * (c.d / kGroup);
+}
+
+// Two e4m3 bytes (low, high) as fp16, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    return h;
+}
+// The eight e2m1 codes of a word as four fp16 pairs (low nibble of a byte = low half), exact.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
+    return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// New tokens of one sequence in an append call; n = 0 where there are none or they cannot be
+// written (then *bad says so).
+struct NewTokens {
+    int first, n, row;  // first position, tokens, row of the first token in k and v
+};
+__device__ __forceinline__ NewTokens new_tokens(const View& c, const int* __restrict__ cu,
+                                                const int* __restrict__ start, int total, int i,
+                                                bool* bad) {
+    NewTokens t;
+    t.row = __ldg(cu + i);
+    const int end = __ldg(cu + i + 1);
+    t.first = __ldg(start + i);
+    const bool range_ok = t.row >= 0 && end >= t.row && end <= total;
+    t.n = range_ok ? end - t.row : 0;
+    bool wrong = !range_ok;
+    if (t.n > 0 && (t.first < 0 || t.first > __ldg(c.lengths + i) ||
+                    (long long)t.first + t.n > (long long)c.max_blocks * c.chunk)) {
+        wrong = true;
+        t.n = 0;
+    }
+    *bad = wrong;
+    return t;
+}
+
+// ---------------------------------------------------------------------------------------
+// Launchers.  Each returns cudaGetLastError() of its launches.
+
+struct AppendArgs {
+    const __nv_bfloat16 *k, *v;
+    const int *cu, *start;
+    int total;
+    __nv_bfloat16 *k_held, *v_held;  // nullptr: not wanted
+};
+cudaError_t launch_append(const View& c, const AppendArgs& a, cudaStream_t st);
+
+cudaError_t launch_reserve(const View& c, const int* upto, int* ws, cudaStream_t st);
+cudaError_t launch_fork(const View& c, const int* src, const int* dst, int n, int* ws, cudaStream_t st);
+cudaError_t launch_free(const View& c, const int* seqs, int n, cudaStream_t st);
+cudaError_t launch_compact(const View& c, const View& into, int* ws, cudaStream_t st);
+// int32 words of workspace that the page operators need.
+inline size_t page_ws_words(int pages, int seqs) { return 64 + 2 * (size_t)pages + 4 * (size_t)seqs; }
+
+// One decode call.  A row is the (up to kRowHeads) query heads of one KV head of one sequence
+// that are attended together.
+constexpr int kRowHeads = 8;
+struct DecodeArgs {
+    const __nv_bfloat16* q;
+    int hq, group, topk;
+    int hgroups;     // rows per (sequence, KV head): ceil(group / kRowHeads)
+    int rows;        // seqs * hkv * hgroups
+    int max_items;   // most blocks of one row's list
+    float scale_log2;  // softmax scale * log2 e * 2^k_exp
+    __nv_bfloat16* out;
+    float* lse;
+};
+struct DecodeWs {
+    int2* items;   // [rows, max_items]: (block, heads that attend to it), ascending blocks
+    int* counts;   // [rows]: items of each row
+};
+cudaError_t launch_decode(const View& c, const DecodeArgs& a, const DecodeWs& ws, cudaStream_t st);
+
+}  // namespace cache
+}  // namespace moba

@@ -707,6 +707,7 @@ const char* moba_status_string(moba_status s) {
         case MOBA_ERR_WORKSPACE: return "MOBA_ERR_WORKSPACE";
         case MOBA_ERR_CUDA: return "MOBA_ERR_CUDA";
         case MOBA_ERR_DEVICE_TIMEOUT: return "MOBA_ERR_DEVICE_TIMEOUT";
+        case MOBA_ERR_NO_PAGES: return "MOBA_ERR_NO_PAGES";
     }
     return "MOBA_ERR_UNKNOWN";
 }

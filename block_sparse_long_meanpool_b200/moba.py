@@ -30,6 +30,15 @@ EXPORTS = (
     "moba_decode_workspace_size",
     "moba_decode_fwd",
     "moba_decode_minmax_fwd",
+    "moba_cache_workspace_size",
+    "moba_cache_reserve",
+    "moba_cache_append",
+    "moba_cache_decode_workspace_size",
+    "moba_cache_decode",
+    "moba_cache_fork",
+    "moba_cache_free",
+    "moba_cache_compact",
+    "moba_cache_status",
     "moba_device_status",
     "moba_device_status_noalloc",
     "moba_selftest_timeout",
@@ -38,7 +47,7 @@ EXPORTS = (
 )
 
 # moba_status codes
-OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT = range(6)
+OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT, ERR_NO_PAGES = range(7)
 
 # moba_run_info event slots
 EV_BEGIN, EV_MEANS_DONE, EV_GATE_DONE, EV_WAVE0 = 0, 1, 2, 3
@@ -59,6 +68,28 @@ class MobaParams(ctypes.Structure):
         ("softmax_scale", ctypes.c_float),
         ("wave_tokens", ctypes.c_int),
         ("gate", ctypes.c_int),
+    ]
+
+
+class MobaCache(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int),
+        ("num_seqs", ctypes.c_int),
+        ("max_blocks", ctypes.c_int),
+        ("num_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("chunk_size", ctypes.c_int),
+        ("k_exp", ctypes.c_int),
+        ("v_exp", ctypes.c_int),
+        ("k_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("k_mean", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("refs", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
     ]
 
 
@@ -119,6 +150,26 @@ def load_library(path=LIB_PATH):
     lib.moba_decode_fwd.restype = ctypes.c_int
     lib.moba_decode_minmax_fwd.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp, vp, vp]
     lib.moba_decode_minmax_fwd.restype = ctypes.c_int
+    C = ctypes.POINTER(MobaCache)
+    lib.moba_cache_workspace_size.argtypes = [C]
+    lib.moba_cache_workspace_size.restype = ctypes.c_size_t
+    lib.moba_cache_reserve.argtypes = [C, vp, vp, ctypes.c_size_t, vp]
+    lib.moba_cache_reserve.restype = ctypes.c_int
+    lib.moba_cache_append.argtypes = [C, vp, vp, vp, vp, ctypes.c_int, vp, vp, vp]
+    lib.moba_cache_append.restype = ctypes.c_int
+    lib.moba_cache_decode_workspace_size.argtypes = [C, ctypes.c_int, ctypes.c_int]
+    lib.moba_cache_decode_workspace_size.restype = ctypes.c_size_t
+    lib.moba_cache_decode.argtypes = [C, vp, ctypes.c_int, ctypes.c_int, ctypes.c_float, vp, ctypes.c_size_t, vp, vp,
+                                      vp]
+    lib.moba_cache_decode.restype = ctypes.c_int
+    lib.moba_cache_fork.argtypes = [C, vp, vp, ctypes.c_int, vp, ctypes.c_size_t, vp]
+    lib.moba_cache_fork.restype = ctypes.c_int
+    lib.moba_cache_free.argtypes = [C, vp, ctypes.c_int, vp]
+    lib.moba_cache_free.restype = ctypes.c_int
+    lib.moba_cache_compact.argtypes = [C, C, vp, ctypes.c_size_t, vp]
+    lib.moba_cache_compact.restype = ctypes.c_int
+    lib.moba_cache_status.argtypes = [C, vp]
+    lib.moba_cache_status.restype = ctypes.c_int
     lib.moba_device_status.argtypes = [P, vp, vp]
     lib.moba_device_status.restype = ctypes.c_int
     lib.moba_device_status_noalloc.argtypes = [vp]

@@ -53,7 +53,8 @@ typedef enum {
     MOBA_ERR_UNSUPPORTED = 2,   /* valid but outside the GPU path limits above */
     MOBA_ERR_WORKSPACE = 3,     /* workspace pointer NULL or smaller than moba_workspace_size */
     MOBA_ERR_CUDA = 4,          /* a CUDA runtime call or kernel launch failed */
-    MOBA_ERR_DEVICE_TIMEOUT = 5 /* a bounded device-side wait gave up (see moba_device_status) */
+    MOBA_ERR_DEVICE_TIMEOUT = 5,/* a bounded device-side wait gave up (see moba_device_status) */
+    MOBA_ERR_NO_PAGES = 6       /* a cache's pool has too few free pages (see moba_cache_status) */
 } moba_status;
 
 typedef struct {
@@ -257,6 +258,112 @@ moba_status moba_decode_minmax_fwd(const moba_params* p, const void* q, const vo
                                    const int* cu_seqlens, const void* k_min, const void* k_max,
                                    void* workspace, size_t workspace_bytes, void* out, float* lse,
                                    void* stream);
+
+/* ---- Paged KV cache in 4 bits ------------------------------------------------------------
+ *
+ * The cache that a serving program appends to, decodes from, forks and frees.  A page holds one
+ * block of the method (chunk_size tokens, every KV head), so the gate's choice names pages.
+ * Keys and values are held in microscaled 4-bit floating point: groups of 16 consecutive
+ * channels of a token share a scale,
+ *     held = e2m1(code) * e4m3(scale) * 2^exp          (exact in bf16)
+ *   k_codes, v_codes    uint8 [num_pages, Hkv, chunk_size, d / 2]: channel 2 i in the low nibble
+ *                       of byte i (sign, two exponent bits, one mantissa bit), 2 i + 1 in the high
+ *   k_scales, v_scales  e4m3 [num_pages, Hkv, chunk_size, d / 16]
+ *   k_mean    fp32 [num_pages, Hkv, d]: the mean of the page's held keys, written when its block
+ *             is complete (the gate reads complete blocks only)
+ *   table     int32 [num_seqs, max_blocks]: the page of each (sequence, block), -1 where none; a
+ *             sequence's pages are its first entries, without gaps
+ *   lengths   int32 [num_seqs]: tokens held
+ *   refs      int32 [num_pages]: how many sequences hold the page, 0 = free
+ *   status    int32 [1]: 0 or the first error that a kernel met (moba_cache_status)
+ * A new cache has table = -1, lengths = refs = status = 0; the pools need no initial contents.
+ * All buffers are the caller's; the four pools, k_mean and every fp32 or bf16 argument are
+ * 16-byte aligned.  The int32 contents are read on the device: an index out of range, a shared
+ * page that would be written or a length that does not fit is reported in `status`, and the
+ * sequence (or, where a call says so, the whole call) is left out; nothing out of bounds is
+ * accessed.  Calls on one cache are ordered by their stream; calls on several streams that
+ * touch the same cache are the caller's to order.
+ *   Limits: head_dim 64 or 128, chunk_size a multiple of 128, num_seqs <= 65535,
+ *   max_blocks * chunk_size < 2^31, |k_exp|, |v_exp| <= 64 (MOBA_ERR_UNSUPPORTED). */
+typedef struct {
+    int num_pages;     /* >= 1 */
+    int num_seqs;      /* slots of sequences, >= 1; an unused slot has length 0 */
+    int max_blocks;    /* width of the table, >= 1 */
+    int num_kv_heads;
+    int head_dim;
+    int chunk_size;    /* tokens per page */
+    int k_exp, v_exp;  /* exponents of the held keys and values; 0 serves values up to 2688 */
+    void *k_codes, *k_scales, *v_codes, *v_scales;
+    float* k_mean;
+    int *table, *lengths, *refs, *status;
+} moba_cache;
+
+/* Bytes of workspace moba_cache_reserve, moba_cache_fork and moba_cache_compact need (compact: of
+ * its source); 0 when the cache is invalid. */
+size_t moba_cache_workspace_size(const moba_cache* c);
+
+/* Pages for tokens to come: sequence i holds pages for positions below upto[i] afterwards
+ * (pages that it has stay).  The lowest free pages are taken, in the order of sequences and
+ * blocks.  All or nothing: too few free pages leave everything as it was (MOBA_ERR_NO_PAGES).
+ *   upto  int32 [num_seqs] device */
+moba_status moba_cache_reserve(const moba_cache* c, const int* upto, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Writes new tokens.  Sequence i's rows cu_new[i] .. cu_new[i+1]-1 of k and v go to positions
+ * start[i], start[i]+1, ...; its length becomes start[i] + their number (start[i] <= its length:
+ * a smaller one takes tokens back first).  A sequence without new rows is left as it is.  Its
+ * pages must be there (moba_cache_reserve) and be its own (refs 1).
+ *   quantisation, per 16 channels of x * 2^-exp: scale = e4m3(min(max|x| / 6, 448)), code =
+ *   e2m1(x / scale), both to nearest, ties to even, saturating; scale 0 gives codes 0; a NaN in
+ *   the group gives scale NaN and codes 0.  k_mean of a completed block is the mean of its held
+ *   keys, whatever the calls that wrote them.
+ *   k, v            bf16 [new_tokens, Hkv, d] device
+ *   cu_new          int32 [num_seqs + 1] device, start int32 [num_seqs] device
+ *   k_held, v_held  bf16 [new_tokens, Hkv, d] device or NULL: receive the values as held (for the
+ *                   attention of the prompt itself) */
+moba_status moba_cache_append(const moba_cache* c, const void* k, const void* v, const int* cu_new,
+                              const int* start, int new_tokens, void* k_held, void* v_held, void* stream);
+
+/* The decode step over the cache: one new query per sequence at its last held token, as
+ * moba_decode_fwd over the held keys and values.  topk >= 1 counts the own block and routes the
+ * topk - 1 best earlier blocks by q . k_mean (ties to the lower index); topk = 0 attends to
+ * every block (the paper decodes with full attention).
+ *   q           bf16 [num_seqs, Hq, d]; an empty sequence yields out = 0, lse = -inf
+ *   workspace   moba_cache_decode_workspace_size bytes, 256-byte aligned, any contents
+ *   out         bf16 [num_seqs, Hq, d]; lse fp32 [Hq, num_seqs] (natural log, scale included)
+ * softmax_scale <= 0 means 1/sqrt(d).  A page of the table that is out of range counts as no
+ * tokens and is reported. */
+size_t moba_cache_decode_workspace_size(const moba_cache* c, int num_q_heads, int topk);
+moba_status moba_cache_decode(const moba_cache* c, const void* q, int num_q_heads, int topk,
+                              float softmax_scale, void* workspace, size_t workspace_bytes, void* out,
+                              float* lse, void* stream);
+
+/* Slot dst[i] becomes a copy of slot src[i]: it shares the full pages (refs + 1), and the tokens
+ * of a partial last page are copied to a page of its own, the lowest free one in the order of i.
+ * A source may be forked several times in a call; a destination must be an unused slot (length
+ * 0, no pages) and be named once.  All or nothing.
+ *   src, dst  int32 [n] device, n >= 0 */
+moba_status moba_cache_fork(const moba_cache* c, const int* src, const int* dst, int n, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Empties slots: every page that a slot holds loses a reference, its table row becomes -1 and its
+ * length 0.  Freeing an unused slot, or a slot twice, does nothing more.
+ *   seqs  int32 [n] device, n >= 0 */
+moba_status moba_cache_free(const moba_cache* c, const int* seqs, int n, void* stream);
+
+/* Packs the pages in use (refs > 0) of c, in ascending order, into the first pages of another
+ * cache `into`, and writes its table, lengths and refs to match: the same sequences in a pool
+ * without holes, smaller or larger.  Both have the same heads, head_dim, chunk_size, exponents,
+ * num_seqs and max_blocks, and no buffer in common.  What `into` held is lost; its pages behind
+ * the packed ones keep their contents.  All or nothing: too few pages in `into` leave it as it
+ * was (MOBA_ERR_NO_PAGES in c's status).  c itself is only read. */
+moba_status moba_cache_compact(const moba_cache* c, const moba_cache* into, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Reads (synchronously, on `stream`) and clears the cache's status word: MOBA_OK,
+ * MOBA_ERR_INVALID_ARG (contents of table, lengths or an index argument), MOBA_ERR_NO_PAGES or
+ * MOBA_ERR_DEVICE_TIMEOUT. */
+moba_status moba_cache_status(const moba_cache* c, void* stream);
 
 /* ---- Self-test of the bounded device waits (no counterpart in the paper) ---------------
  *

@@ -1,0 +1,158 @@
+"""Refusals of the 4-bit cache's calls, and its sizes: host checks only (CPU)."""
+
+import ctypes
+
+import pytest
+import torch
+
+from block_sparse_long_meanpool_b200 import build, cache, moba
+
+FAKE = 1 << 20  # an aligned address that no refused call touches
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return moba.load_library()
+
+
+def desc(**kw):
+    base = dict(num_pages=10, num_seqs=3, max_blocks=4, num_kv_heads=2, head_dim=64, chunk_size=128, k_exp=0, v_exp=0,
+                k_codes=FAKE, k_scales=FAKE, v_codes=FAKE, v_scales=FAKE, k_mean=FAKE, table=FAKE, lengths=FAKE,
+                refs=FAKE, status=FAKE)
+    base.update(kw)
+    return moba.MobaCache(**base)
+
+
+BAD_SHAPES = [
+    (dict(num_pages=0), moba.ERR_INVALID_ARG),
+    (dict(num_seqs=0), moba.ERR_INVALID_ARG),
+    (dict(max_blocks=0), moba.ERR_INVALID_ARG),
+    (dict(num_kv_heads=0), moba.ERR_INVALID_ARG),
+    (dict(num_pages=-1), moba.ERR_INVALID_ARG),
+    (dict(chunk_size=0), moba.ERR_INVALID_ARG),
+    (dict(head_dim=96), moba.ERR_UNSUPPORTED),
+    (dict(chunk_size=64), moba.ERR_UNSUPPORTED),
+    (dict(chunk_size=2 << 20), moba.ERR_UNSUPPORTED),
+    (dict(num_seqs=65536), moba.ERR_UNSUPPORTED),
+    (dict(max_blocks=1 << 24), moba.ERR_UNSUPPORTED),
+    (dict(k_exp=65), moba.ERR_UNSUPPORTED),
+    (dict(v_exp=-65), moba.ERR_UNSUPPORTED),
+]
+
+
+def calls(lib, c, n=1 << 30):
+    """Every call on the cache, otherwise well formed; none gets past the host checks of a bad cache."""
+    r, ws = ctypes.byref(c), FAKE
+    good = ctypes.byref(desc(k_codes=2 * FAKE, k_scales=2 * FAKE, v_codes=2 * FAKE, v_scales=2 * FAKE, k_mean=2 * FAKE,
+                             table=2 * FAKE, lengths=2 * FAKE, refs=2 * FAKE))
+    return [lib.moba_cache_reserve(r, FAKE, ws, n, None),
+            lib.moba_cache_append(r, FAKE, FAKE, FAKE, FAKE, 5, None, None, None),
+            lib.moba_cache_decode(r, FAKE, 4, 3, 0.0, ws, n, FAKE, FAKE, None),
+            lib.moba_cache_fork(r, FAKE, FAKE, 1, ws, n, None),
+            lib.moba_cache_free(r, FAKE, 1, None),
+            lib.moba_cache_compact(r, good, ws, n, None),
+            lib.moba_cache_status(r, None)]
+
+
+@pytest.mark.parametrize("kw,status", BAD_SHAPES)
+def test_bad_shapes_are_refused_by_every_call(lib, kw, status):
+    c = desc(**kw)
+    assert lib.moba_cache_workspace_size(ctypes.byref(c)) == 0
+    assert lib.moba_cache_decode_workspace_size(ctypes.byref(c), 4, 3) == 0
+    assert calls(lib, c) == [status] * 7
+    assert lib.moba_last_error()
+
+
+@pytest.mark.parametrize("name", ["k_codes", "k_scales", "v_codes", "v_scales", "k_mean", "table", "lengths", "refs",
+                                  "status"])
+def test_missing_and_misaligned_buffers_are_refused(lib, name):
+    assert calls(lib, desc(**{name: None})) == [moba.ERR_INVALID_ARG] * 7
+    assert b"NULL" in lib.moba_last_error()
+    assert calls(lib, desc(**{name: FAKE + 2})) == [moba.ERR_INVALID_ARG] * 7
+    assert b"aligned" in lib.moba_last_error()
+
+
+def test_bad_arguments_are_refused(lib):
+    c = desc()
+    r, I, U, W = ctypes.byref(c), moba.ERR_INVALID_ARG, moba.ERR_UNSUPPORTED, moba.ERR_WORKSPACE
+    need = lib.moba_cache_workspace_size(r)
+    dneed = lib.moba_cache_decode_workspace_size(r, 4, 3)
+    assert need > 0 and dneed > 0
+    # workspaces: absent, short, misaligned
+    for ws, n in ((None, need), (FAKE, need - 1), (FAKE + 16, need)):
+        assert lib.moba_cache_reserve(r, FAKE, ws, n, None) == W
+        assert lib.moba_cache_fork(r, FAKE, FAKE, 1, ws, n, None) == W
+        into = ctypes.byref(desc(k_codes=2 * FAKE, k_scales=2 * FAKE, v_codes=2 * FAKE, v_scales=2 * FAKE,
+                                 k_mean=2 * FAKE, table=2 * FAKE, lengths=2 * FAKE, refs=2 * FAKE))
+        assert lib.moba_cache_compact(r, into, ws, n, None) == W
+    for ws, n in ((None, dneed), (FAKE, dneed - 1), (FAKE + 16, dneed)):
+        assert lib.moba_cache_decode(r, FAKE, 4, 3, 0.0, ws, n, FAKE, FAKE, None) == W
+    n = 1 << 30
+    # null pointers
+    assert lib.moba_cache_reserve(r, None, FAKE, n, None) == I
+    assert lib.moba_cache_append(r, None, FAKE, FAKE, FAKE, 5, None, None, None) == I
+    assert lib.moba_cache_append(r, FAKE, FAKE, FAKE, None, 5, None, None, None) == I
+    assert lib.moba_cache_append(r, FAKE, FAKE, FAKE, FAKE, 5, FAKE, None, None) == I
+    assert lib.moba_cache_decode(r, None, 4, 3, 0.0, FAKE, n, FAKE, FAKE, None) == I
+    assert lib.moba_cache_decode(r, FAKE, 4, 3, 0.0, FAKE, n, FAKE, None, None) == I
+    assert lib.moba_cache_fork(r, FAKE, None, 1, FAKE, n, None) == I
+    assert lib.moba_cache_free(r, None, 1, None) == I
+    # counts, heads, topk, scale, alignment
+    assert lib.moba_cache_append(r, FAKE, FAKE, FAKE, FAKE, -1, None, None, None) == I
+    assert lib.moba_cache_append(r, FAKE + 8, FAKE, FAKE, FAKE, 5, None, None, None) == I
+    assert lib.moba_cache_fork(r, FAKE, FAKE, -1, FAKE, n, None) == I
+    assert lib.moba_cache_fork(r, FAKE, FAKE, 4, FAKE, n, None) == I  # more than num_seqs
+    assert lib.moba_cache_free(r, FAKE, -1, None) == I
+    for hq, topk, want in ((3, 3, I), (0, 3, I), (-2, 3, I), (4, -1, I), (4, 33, U)):
+        assert lib.moba_cache_decode(r, FAKE, hq, topk, 0.0, FAKE, n, FAKE, FAKE, None) == want
+        assert lib.moba_cache_decode_workspace_size(r, hq, topk) == 0
+    for scale in (float("nan"), float("inf")):
+        assert lib.moba_cache_decode(r, FAKE, 4, 3, scale, FAKE, n, FAKE, FAKE, None) == I
+    assert lib.moba_cache_decode(r, FAKE + 8, 4, 3, 0.0, FAKE, n, FAKE, FAKE, None) == I
+    # compact: another geometry, a shared buffer
+    other = dict(k_codes=2 * FAKE, k_scales=2 * FAKE, v_codes=2 * FAKE, v_scales=2 * FAKE, k_mean=2 * FAKE,
+                 table=2 * FAKE, lengths=2 * FAKE, refs=2 * FAKE)
+    for kw in (dict(other, head_dim=128), dict(other, chunk_size=256), dict(other, num_kv_heads=1), dict(other, k_exp=1),
+               dict(other, num_seqs=4), dict(other, max_blocks=5), dict(other, table=FAKE), dict(other, v_codes=FAKE)):
+        assert lib.moba_cache_compact(r, ctypes.byref(desc(**kw)), FAKE, n, None) == I, kw
+    assert lib.moba_cache_compact(r, None, FAKE, n, None) == I
+
+
+def test_empty_calls_do_nothing(lib):
+    r = ctypes.byref(desc())
+    assert lib.moba_cache_append(r, None, None, None, None, 0, None, None, None) == moba.OK
+    assert lib.moba_cache_fork(r, None, None, 0, None, 0, None) == moba.OK
+    assert lib.moba_cache_free(r, None, 0, None) == moba.OK
+
+
+def test_status_name(lib):
+    assert lib.moba_status_string(moba.ERR_NO_PAGES) == b"MOBA_ERR_NO_PAGES"
+
+
+def test_binding_refuses_host_tensors_and_wrong_buffers(lib):
+    def bufs(device="cpu", **kw):
+        b = dict(k_codes=torch.zeros((4, 2, 128, 32), dtype=torch.uint8, device=device),
+                 k_scales=torch.zeros((4, 2, 128, 4), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn),
+                 v_codes=torch.zeros((4, 2, 128, 32), dtype=torch.uint8, device=device),
+                 v_scales=torch.zeros((4, 2, 128, 4), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn),
+                 k_mean=torch.zeros((4, 2, 64), device=device), refs=torch.zeros(4, dtype=torch.int32, device=device),
+                 table=torch.full((3, 2), -1, dtype=torch.int32, device=device),
+                 lengths=torch.zeros(3, dtype=torch.int32, device=device))
+        b.update(kw)
+        return b
+
+    with pytest.raises(ValueError, match="CUDA"):
+        cache.KVCache.from_tensors(**bufs())
+    with pytest.raises(ValueError, match="k_codes"):
+        cache.KVCache.from_tensors(**bufs(k_codes=torch.zeros(4, 2, 128)))
+    with pytest.raises(ValueError, match=">= 1"):
+        cache.KVCache(0, 1, 1, 1, 64, 128, device="cpu")
+    with pytest.raises(ValueError, match="multiple"):
+        cache.KVCache(1, 1, 1, 1, 60, 128, device="cpu")
+    x = torch.zeros((2, 3), dtype=torch.int32)
+    for shape, dtype, t in (((2, 3), torch.int64, x), ((3, 2), torch.int32, x), ((3, 2), torch.int32, x.t())):
+        with pytest.raises(ValueError, match="name"):
+            cache._need(t, "name", shape, dtype, x.device)
+    with pytest.raises(ValueError):
+        cache._need(x, "name", (2, 3), torch.int32, torch.device("meta"))

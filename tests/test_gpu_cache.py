@@ -1,0 +1,696 @@
+"""The paged 4-bit cache on the GPU, against the plain model in float64 (tests/cache_model.py).
+
+Codes, scales, held values, tables, references and lengths have to be the model's exactly: every
+rounding of the quantisation is decided exactly.  k_mean and the decode step are held to bounds
+from the arithmetic (mean_bound, decode_bounds)."""
+
+import numpy as np
+import pytest
+import torch
+
+import cache_model as M
+from block_sparse_long_meanpool_b200 import cache, moba
+from block_sparse_long_meanpool_b200 import (KVCache, cache_append, cache_compact, cache_decode, cache_fork, cache_free,
+                                             cache_reserve, cache_status)
+
+pytestmark = pytest.mark.gpu
+
+
+def ints(x):
+    return torch.tensor(list(map(int, x)), dtype=torch.int32, device="cuda")
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+def bf16(x):
+    return torch.tensor(np.asarray(x)).bfloat16()
+
+
+def pair(pages, seqs, blocks, heads, d, chunk, garbage=True, **kw):
+    """An empty cache and its model.  The pools hold NaN scales and the largest codes, which nothing may read."""
+    c = KVCache(pages, seqs, blocks, heads, d, chunk, **kw)
+    for t in (c.k_codes, c.k_scales, c.v_codes, c.v_scales):
+        t.view(torch.uint8).fill_(0xff if garbage else 0)
+    c.k_mean.fill_(float("nan") if garbage else 0.0)
+    return c, M.Model(pages, seqs, blocks, heads, d, chunk, **kw)
+
+
+def unpack(codes):
+    b = codes.cpu().numpy().astype(np.int64)
+    return np.stack([b & 15, b >> 4], -1).reshape(b.shape[:-1] + (-1,))
+
+
+def mean_bound(m, page):
+    """fp32 sum of chunk held keys in any order, and one division."""
+    return (m.chunk + 2) * 2.0 ** -24 * np.abs(m.held(0, page)).mean(1)
+
+
+def same(c, m):
+    """The cache's tables and every held token are the model's, bit for bit; means of complete blocks are near."""
+    np.testing.assert_array_equal(c.lengths.cpu().numpy(), m.lengths)
+    np.testing.assert_array_equal(c.table.cpu().numpy(), m.table)
+    np.testing.assert_array_equal(c.refs.cpu().numpy(), m.refs)
+    for x, (codes, scales) in enumerate(((c.k_codes, c.k_scales), (c.v_codes, c.v_scales))):
+        got_c, got_s = unpack(codes), scales.view(torch.uint8).cpu().numpy()
+        for i in range(m.ns):
+            for j in range(-(-int(m.lengths[i]) // m.chunk)):
+                p, n = m.table[i, j], min(m.chunk, int(m.lengths[i]) - j * m.chunk)
+                np.testing.assert_array_equal(got_c[p, :, :n], m.codes[x][p, :, :n])
+                np.testing.assert_array_equal(got_s[p, :, :n], m.scales[x][p, :, :n])
+    mean = host(c.k_mean)
+    for i in range(m.ns):
+        for p in m.table[i, :int(m.lengths[i]) // m.chunk]:
+            assert (np.abs(mean[p] - m.mean[p]) <= mean_bound(m, p)).all()
+
+
+def decode_bounds(c, m, q, topk, scale=None):
+    """Model outputs and error bounds.  A score is an fp32 sum of d exact products in any order, with
+    truncating additions allowed for: (d + 16) 2^-22 of the largest sum |q k| covers it, its scaling and the
+    exponential's argument; p is rounded to fp16 (2^-11, and 2^-25 absolute below fp16's normal range) or
+    kept wider; n terms are added in fp32; the output is rounded to bf16 (2^-8)."""
+    out, lse, gap, pv, qk = m.decode(q, topk, scale)
+    n, d = max(1, int(m.lengths.max())), m.d
+    e = (d + 16) * 2.0 ** -22 * qk
+    vmax = max([np.abs(np.nan_to_num(m.held(1, p))).max() for p in np.flatnonzero(m.refs > 0)] + [0])
+    tol = 2.0 ** -8 * np.abs(out) + (4 * e[..., None] + 2.0 ** -11 + n * 2.0 ** -22) * pv + n * 2.0 ** -25 * vmax
+    ltol = (e + 2.0 ** -20 + n * 2.0 ** -23).T + 2.0 ** -21 * np.abs(np.where(np.isinf(lse), 0, lse))
+    # Rows whose choice the scores decide: the gap passes two score errors.  A score is d products q m added in
+    # fp32, rounded to nearest: whatever the order, no product passes more than d roundings of 2^-24 of the
+    # partial sums, which sum |q m| bounds, so an error is at most d 2^-24 sum |q m|; the stored mean is off
+    # by (chunk + 2) 2^-24 of its keys' mean magnitude at most, in practice by its last rounding: 2^-24 more.
+    sure = gap > 2 * (d + 1) * 2.0 ** -24
+    return out, lse, tol, ltol, sure
+
+
+def check_decode(c, m, q, topk, scale=None, got=None):
+    qt = bf16(q).cuda()
+    o, l = got or cache_decode(c, qt, topk, softmax_scale=scale)
+    out, lse, tol, ltol, sure = decode_bounds(c, m, host(qt), topk, scale)
+    assert sure.all(), "the inputs leave a gate choice to rounding"
+    o, l = host(o), host(l)
+    assert np.isfinite(o).all()
+    assert (np.abs(o - out) <= tol).all(), np.max(np.abs(o - out) - tol)
+    empty = np.isinf(lse)
+    np.testing.assert_array_equal(np.isneginf(l), empty)
+    assert (np.abs(l[~empty] - lse[~empty]) <= ltol[~empty]).all()
+    assert not o[m.lengths == 0].any()
+
+
+def fill(c, m, rng, lengths, spread=1.0, v_spread=1.0):
+    """Prompts of these lengths, their blocks' keys offset so that the gate has a choice."""
+    assert m.reserve(lengths)
+    cache_reserve(c, ints(lengths))
+    n = int(sum(lengths))
+    cu = np.concatenate([[0], np.cumsum(lengths)]).astype(int)
+    k, v = (rng.standard_normal((n, m.h, m.d)) * s for s in (spread, v_spread))
+    for i in range(m.ns):
+        for j in range(-(-int(lengths[i]) // m.chunk)):
+            rows = slice(cu[i] + j * m.chunk, min(cu[i + 1], cu[i] + (j + 1) * m.chunk))
+            k[rows] += 0.5 * spread * rng.standard_normal((1, m.h, m.d))
+    kt, vt = bf16(k), bf16(v)
+    m.append(kt.double().numpy(), vt.double().numpy(), cu, np.zeros(m.ns, int))
+    cache_append(c, kt.cuda(), vt.cuda(), ints(cu), ints([0] * m.ns))
+
+
+# ---- append -------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("d,heads,chunk,exp,steps", [
+    (64, 1, 128, 0, [[1, 0, 5]]),
+    (128, 2, 128, 0, [[200, 1, 128], [56, 0, 1], [1, 127, 127]]),
+    (64, 3, 256, -4, [[255, 256, 257], [1, 1, 255], [3, 300, 0]]),
+    (128, 8, 384, 3, [[0, 383, 64], [700, 2, 65]]),
+    (64, 5, 128, 0, [[1, 1, 1]] * 3),
+])
+def test_append_is_the_model_exactly(d, heads, chunk, exp, steps):
+    rng = np.random.default_rng(10)
+    c, m = pair(20, 3, 8, heads, d, chunk, k_exp=exp, v_exp=exp - 1)
+    for new in steps:
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(int)
+        start = m.lengths.copy()
+        k, v = (bf16(rng.standard_normal((cu[-1], heads, d)) * 2.0 ** (exp + rng.integers(-3, 3))) for _ in "kv")
+        assert m.reserve(m.lengths + new)
+        want = m.append(k.double().numpy(), v.double().numpy(), cu, start)
+        cache_reserve(c, ints(start + new))
+        held = cache_append(c, k.cuda(), v.cuda(), ints(cu), ints(start), return_held=True)
+        for h, w in zip(held, want):
+            np.testing.assert_array_equal(host(h), w)
+        same(c, m)
+    cache_status(c)
+
+
+def test_every_bf16_value_at_many_scales():
+    """Every bf16 bit pattern, with the group's largest magnitude swept over every e4m3 scale and beyond both
+    ends: zeros, ties of the grid, subnormals, infinities and NaN."""
+    top = np.concatenate([6 * M.E4M3, [1e-5, 2.0 ** -10 * 6 / 2, 2 * 448 * 6, 3e38]])
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    heads, d, chunk = 2, 128, 128
+    x = torch.zeros((len(top), 65536 // 8, 16), dtype=torch.bfloat16)  # 8 of the values, the largest, zeros
+    x[:, :, :8] = every.view(-1, 8)
+    big = bf16(top)[:, None].expand(-1, 8192)
+    finite = x[:, :, :8].float().abs().nan_to_num(nan=0.0, posinf=0.0).amax(-1)
+    # values above the largest one would set the scale themselves: keep those groups as they are
+    x[:, :, 9] = torch.where(finite <= big.float(), big, torch.zeros_like(big))
+    x[:, :, 12] = -x[:, :, 9] * 0.75
+    x = x.reshape(-1, heads, d)
+    x = x[torch.randperm(len(x), generator=torch.Generator().manual_seed(4))[:chunk * 500]]
+    c = KVCache(500, 1, 500, heads, d, chunk)
+    cache_reserve(c, ints([len(x)]))
+    hk, hv = cache_append(c, x.cuda(), x.flip(0).contiguous().cuda(), ints([0, len(x)]), ints([0]), return_held=True)
+    cache_status(c)
+    codes, scales = M.quantise(x.double().numpy())
+    np.testing.assert_array_equal(unpack(c.k_codes[c.table[0].long()].transpose(1, 2).reshape(-1, heads, d // 2)), codes)
+    np.testing.assert_array_equal(c.k_scales.view(torch.uint8)[c.table[0].long()].transpose(1, 2).reshape(
+        -1, heads, d // 16).cpu().numpy(), scales)
+    want = M.values(codes, scales)
+    np.testing.assert_array_equal(host(hk), want)
+    np.testing.assert_array_equal(host(hv), want[::-1])
+
+
+def test_pieces_write_what_one_call_writes():
+    """Pools, means and lengths are bit for bit the same however the tokens are cut into calls."""
+    rng = np.random.default_rng(11)
+    n, heads, d, chunk = 900, 2, 64, 128
+    k, v = (bf16(rng.standard_normal((n, heads, d))).cuda() for _ in "kv")
+    got = []
+    for cuts in ([n], [1] * 130 + [n - 130], [127, 2, 255, 129, 387], [64] * 14 + [4]):
+        c = KVCache(8, 1, 8, heads, d, chunk)
+        for t in (c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.k_mean):
+            t.view(torch.uint8).zero_()
+        cache_reserve(c, ints([n]))
+        a = 0
+        for x in cuts:
+            cache_append(c, k[a:a + x].contiguous(), v[a:a + x].contiguous(), ints([0, x]), ints([a]))
+            a += x
+        cache_status(c)
+        got.append([t.view(torch.uint8).clone() for t in (c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.k_mean)] +
+                   [c.lengths.clone()])
+    for other in got[1:]:
+        for x, y in zip(got[0], other):
+            assert torch.equal(x, y)
+
+
+def test_append_takes_tokens_back_and_refuses_gaps():
+    rng = np.random.default_rng(12)
+    c, m = pair(12, 2, 4, 1, 64, 128)
+    fill(c, m, rng, [300, 200])
+    k, v = (bf16(rng.standard_normal((40, 1, 64))) for _ in "kv")
+    # sequence 0 goes on from position 120 (three blocks held, two kept), sequence 1 stays
+    m.append(k.double().numpy(), v.double().numpy(), [0, 40, 40], [120, 7])
+    cache_append(c, k.cuda(), v.cuda(), ints([0, 40, 40]), ints([120, 7]))
+    cache_status(c)
+    same(c, m)
+    lengths = c.lengths.clone()
+    before = [t.view(torch.uint8).clone() for t in (c.k_codes, c.v_codes, c.k_scales, c.v_scales)]
+    for start in ([161, 200], [-1, 200], [160, 201], [160, 400], [2 ** 31 - 30, 200]):
+        cache_append(c, k.cuda(), v.cuda(), ints([0, 0, 40] if start[0] == 160 else [0, 40, 40]), ints(start))
+        with pytest.raises(moba.MobaError) as e:
+            cache_status(c)
+        assert e.value.status == moba.ERR_INVALID_ARG
+        assert torch.equal(c.lengths, lengths)
+    for cu in ([0, 41, 41], [-1, 40, 40], [5, 3, 3], [0, 40, 41]):
+        cache_append(c, k.cuda(), v.cuda(), ints(cu), ints([2 ** 30, 2 ** 30]))
+        with pytest.raises(moba.MobaError):
+            cache_status(c)
+    for a, b in zip(before, (c.k_codes, c.v_codes, c.k_scales, c.v_scales)):
+        assert torch.equal(a, b.view(torch.uint8))
+    cache_status(c)
+
+
+def test_append_needs_pages_of_its_own():
+    """No page, a page out of range and a shared page are reported; the length stays."""
+    rng = np.random.default_rng(13)
+    k, v = (bf16(rng.standard_normal((10, 1, 64))).cuda() for _ in "kv")
+    for spoil in ("none", "range", "negative", "shared", "free"):
+        c, m = pair(4, 2, 2, 1, 64, 128)
+        fill(c, m, rng, [5, 5])
+        if spoil == "none":
+            c.table[0, 0] = -1
+        elif spoil == "range":
+            c.table[0, 0] = 4
+        elif spoil == "negative":
+            c.table[0, 0] = -2 ** 31
+        else:
+            c.refs[m.table[0, 0]] = 2 if spoil == "shared" else 0
+        pools = [t.view(torch.uint8).clone() for t in (c.k_codes, c.v_codes)]
+        cache_append(c, k, v, ints([0, 10, 10]), ints([5, 5]))
+        with pytest.raises(moba.MobaError):
+            cache_status(c)
+        assert c.lengths.tolist() == [5, 5]
+        for a, b in zip(pools, (c.k_codes, c.v_codes)):
+            assert torch.equal(a, b)
+
+
+# ---- decode -------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("d,heads,group,chunk,topk,lengths", [
+    (64, 1, 1, 128, 1, [1]),
+    (128, 1, 1, 128, 0, [1, 0, 2, 63, 64, 65, 127, 128, 129]),
+    (64, 4, 1, 256, 3, [1999]),
+    (128, 2, 4, 128, 3, [700, 1337, 128, 1, 0, 390]),
+    (128, 2, 4, 128, 0, [700, 1337, 128, 1, 0, 390]),
+    (64, 2, 3, 384, 2, [2000, 999, 385]),
+    (64, 1, 8, 128, 5, [1500, 640]),
+    (128, 1, 9, 128, 4, [1400, 130]),
+    (64, 2, 20, 128, 0, [333, 700]),
+    (128, 1, 16, 128, 32, [4500]),
+    (64, 3, 2, 128, 32, [5000, 100]),
+    (128, 1, 33, 128, 2, [600]),
+])
+def test_decode_is_the_model(d, heads, group, chunk, topk, lengths):
+    rng = np.random.default_rng(20)
+    blocks = max(-(-n // chunk) for n in lengths) + 1
+    c, m = pair(sum(-(-n // chunk) for n in lengths) + 2, len(lengths), blocks, heads, d, chunk)
+    fill(c, m, rng, lengths)
+    q = rng.standard_normal((len(lengths), heads * group, d))
+    check_decode(c, m, q, topk)
+    cache_status(c)
+
+
+@pytest.mark.parametrize("topk", [0, 3])
+def test_decode_scales_and_magnitudes(topk):
+    """A softmax scale of the caller's, exponents, queries near the ends of bf16's range, heads of zeros."""
+    rng = np.random.default_rng(21)
+    for exp, qs, scale in ((-7, 1.0, None), (9, 1.0, 2.0 ** -9 * 0.1), (0, 1e36, 1e-36), (0, 1e-36, 1e34), (0, 0.0, 1.0),
+                           (0, 30.0, 1.0)):
+        c, m = pair(16, 2, 8, 2, 64, 128, k_exp=exp, v_exp=-exp)
+        fill(c, m, rng, [900, 300], spread=2.0 ** exp, v_spread=2.0 ** -exp)
+        q = rng.standard_normal((2, 4, 64)) * qs
+        q[1, 2] = 0
+        if qs == 0 or topk:
+            q[1, 2] = q[1, 3]  # all scores equal: the choice would be one of ties
+        if qs == 0 and topk:
+            continue
+        check_decode(c, m, q, topk, scale)
+
+
+def test_gate_ties_go_to_the_lower_block():
+    """Blocks of equal keys score equally; the lower ones are taken."""
+    c, m = pair(8, 1, 8, 1, 64, 128)
+    n = 6 * 128 + 3
+    k = np.ones((n, 1, 64))
+    k[3 * 128:4 * 128] = 2.0
+    v = np.repeat(np.arange(n) // 128, 64).reshape(n, 1, 64).astype(float)
+    m.reserve([n])
+    cache_reserve(c, ints([n]))
+    hk, hv = m.append(k, v, [0, n], [0])
+    cache_append(c, bf16(k).cuda(), bf16(v).cuda(), ints([0, n]), ints([0]))
+    # every channel of a block holds one value (1 is held as 6 * 11 / 64: 1/6 is no e4m3 value)
+    kb, vb = hk[::128, 0, 0], hv[::128, 0, 0]
+    o, _ = cache_decode(c, torch.zeros((1, 1, 64), dtype=torch.bfloat16, device="cuda"), 3)
+    # scores 0 everywhere: blocks 0 and 1, and the own block's 3 tokens
+    want = (128 * vb[0] + 128 * vb[1] + 3 * vb[6]) / (2 * 128 + 3)
+    assert np.allclose(host(o), want, rtol=2.0 ** -7)
+    x = 0.01
+    o, _ = cache_decode(c, torch.full((1, 1, 64), x, dtype=torch.bfloat16, device="cuda"), 3)
+    w = np.exp(64 * float(torch.tensor(x).bfloat16()) / 8 * kb)  # the larger block 3, and of the equal ones block 0
+    want = (128 * w[3] * vb[3] + 128 * w[0] * vb[0] + 3 * w[6] * vb[6]) / (128 * w[3] + 128 * w[0] + 3 * w[6])
+    assert np.allclose(host(o), want, rtol=2.0 ** -7)
+
+
+def test_decode_ranks_nan_scores_last_and_keeps_other_rows():
+    """A NaN in one block's keys: its mean ranks behind every other block, other heads and rows do not see it."""
+    rng = np.random.default_rng(22)
+    c, m = pair(16, 2, 8, 2, 64, 128)
+    fill(c, m, rng, [800, 800])
+    page = int(m.table[0, 2])
+    c.k_mean[page, 0] = float("nan")
+    q = rng.standard_normal((2, 2, 64))
+    o, l = cache_decode(c, bf16(q).cuda(), 3)
+    assert torch.isfinite(o).all() and torch.isfinite(l).all()
+    out, lse, tol, ltol, sure = decode_bounds(c, m, host(bf16(q)), 3)
+    keep = [(0, 1), (1, 0), (1, 1)]
+    assert sure[tuple(zip(*keep))].all()
+    for i, h in keep:
+        assert (np.abs(host(o)[i, h] - out[i, h]) <= tol[i, h]).all()
+    # with every earlier block but one taken, the NaN block is the one left out
+    o, l = cache_decode(c, bf16(q).cuda(), 6)
+    s = m.mean[m.table[0, :6], 0] @ host(bf16(q))[0, 0]
+    s[2] = -np.inf
+    keep = sorted(np.argsort(-s)[:5])
+    assert 2 not in keep
+    ks = np.concatenate([m.held(0, m.table[0, j])[0] for j in keep] + [m.held(0, m.table[0, 6])[0, :32]])
+    z = ks @ host(bf16(q))[0, 0] / 8
+    assert abs(host(l)[0, 0] - (z.max() + np.log(np.exp(z - z.max()).sum()))) < 1e-4
+
+
+def test_decode_reports_bad_pages_and_lengths():
+    """A page out of range counts as no tokens, a length out of range as an empty slot; both are reported and
+    the other sequences' results stay."""
+    rng = np.random.default_rng(23)
+    q = bf16(rng.standard_normal((3, 2, 64)))
+    for topk in (0, 3):
+        c, m = pair(24, 3, 6, 1, 64, 128)
+        fill(c, m, rng, [600, 700, 500])
+        good = cache_decode(c, q.cuda(), topk)
+        for bad in (24, -1, 2 ** 31 - 1, -2 ** 31):
+            c.table[0, 4] = bad  # the own block of sequence 0
+            o, l = cache_decode(c, q.cuda(), topk)
+            with pytest.raises(moba.MobaError):
+                cache_status(c)
+            assert torch.isfinite(o).all()
+            assert torch.equal(o[1:], good[0][1:]) and torch.equal(l[:, 1:], good[1][:, 1:])
+            c.table[0, 4] = int(m.table[0, 4])
+        for bad in (-1, 6 * 128 + 1, 2 ** 31 - 1):
+            c.lengths[1] = bad
+            o, l = cache_decode(c, q.cuda(), topk)
+            with pytest.raises(moba.MobaError):
+                cache_status(c)
+            assert not o[1].any() and torch.isneginf(l[:, 1]).all()
+            assert torch.equal(o[::2], good[0][::2]) and torch.equal(l[:, ::2], good[1][:, ::2])
+            c.lengths[1] = 700
+        c.table[2] = -1  # no page at all
+        o, l = cache_decode(c, q.cuda(), topk)
+        assert not o[2].any() and torch.isneginf(l[:, 2]).all()
+        with pytest.raises(moba.MobaError):
+            cache_status(c)
+
+
+def test_decode_far_in_a_large_pool():
+    """Codes behind 2^32 bytes of the pool."""
+    rng = np.random.default_rng(24)
+    heads, d, chunk = 8, 128, 4096
+    pages = 2 ** 32 // (heads * chunk * d // 2) + 3
+    c = KVCache(pages, 1, 3, heads, d, chunk)
+    c.refs[:pages - 3] = 1  # in use by nobody that is asked for
+    n = 2 * chunk + 130
+    cache_reserve(c, ints([n]))
+    assert c.table.tolist() == [[pages - 3, pages - 2, pages - 1]]
+    k, v = (torch.tensor(rng.standard_normal((n, heads, d))).bfloat16().cuda() for _ in "kv")
+    hk, hv = cache_append(c, k, v, ints([0, n]), ints([0]), return_held=True)
+    cache_status(c)
+    q = torch.tensor(rng.standard_normal((1, heads, d))).bfloat16().cuda()
+    o, l = cache_decode(c, q, 0)
+    z = torch.einsum("hd,nhd->hn", q[0].double(), hk.double()) / d ** 0.5
+    want = torch.einsum("hn,nhd->hd", torch.softmax(z, 1), hv.double())
+    mean = hk[:2 * chunk].double().view(2, chunk, heads, d).mean(1)
+    assert (c.k_mean[pages - 3:pages - 1].double() - mean).abs().max() <= (chunk + 2) * 2.0 ** -24 * 4
+    pv = torch.einsum("hn,nhd->hd", torch.softmax(z, 1), hv.double().abs())
+    assert ((o[0].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -10 + n * 2.0 ** -22) * pv).all()
+    assert (l[:, 0].double() - torch.logsumexp(z, 1)).abs().max() < 1e-4
+
+
+# ---- pages --------------------------------------------------------------------------------------
+
+def test_reserve_takes_the_lowest_pages_all_or_none():
+    c, m = pair(9, 3, 5, 1, 64, 128)
+    for upto in ([200, 0, 1], [100, 128, 300], [256, 129, 384]):
+        assert m.reserve(upto)
+        cache_reserve(c, ints(upto))
+        cache_status(c)
+        np.testing.assert_array_equal(c.table.cpu().numpy(), m.table)
+        np.testing.assert_array_equal(c.refs.cpu().numpy(), m.refs)
+    assert not m.reserve([640, 640, 384])
+    cache_reserve(c, ints([640, 640, 384]))
+    with pytest.raises(moba.MobaError) as e:
+        cache_status(c)
+    assert e.value.status == moba.ERR_NO_PAGES
+    for bad in ([-1, 0, 0], [0, 641, 0], [0, 0, 2 ** 31 - 1]):
+        cache_reserve(c, ints(bad))
+        with pytest.raises(moba.MobaError) as e:
+            cache_status(c)
+        assert e.value.status == moba.ERR_INVALID_ARG
+    np.testing.assert_array_equal(c.table.cpu().numpy(), m.table)
+    np.testing.assert_array_equal(c.refs.cpu().numpy(), m.refs)
+    cache_status(c)
+
+
+@pytest.mark.parametrize("seqs,pages", [(3000, 7000), (1, 2500)])
+def test_reserve_over_many_sequences_and_pages(seqs, pages):
+    """More sequences and pages than one pass of the planning block."""
+    rng = np.random.default_rng(30)
+    c, m = pair(pages, seqs, 2000 if seqs == 1 else 4, 1, 64, 128)
+    taken = rng.random(pages) < 0.3
+    m.refs[taken] = 1
+    c.refs.copy_(ints(m.refs))
+    upto = [2000 * 128] if seqs == 1 else rng.integers(0, 129 * 2, seqs)
+    assert m.reserve(upto) == (seqs > 1)
+    cache_reserve(c, ints(upto))
+    np.testing.assert_array_equal(c.table.cpu().numpy(), m.table)
+    np.testing.assert_array_equal(c.refs.cpu().numpy(), m.refs)
+    if seqs > 1:
+        cache_status(c)
+        return
+    with pytest.raises(moba.MobaError):
+        cache_status(c)
+
+
+@pytest.mark.parametrize("d,heads,chunk", [(64, 3, 128), (128, 2, 384)])
+def test_fork_shares_full_pages_and_copies_the_partial_one(d, heads, chunk):
+    rng = np.random.default_rng(31)
+    c, m = pair(40, 9, 6, heads, d, chunk)
+    fill(c, m, rng, [2 * chunk + 37, chunk, 1, 0, 0, 0, 0, 0, 0])
+    pools = {n: getattr(c, n).view(torch.uint8).clone() for n in ("k_codes", "k_scales", "v_codes", "v_scales")}
+    src, dst = [0, 1, 0, 2, 3], [5, 4, 8, 6, 7]
+    assert m.fork(np.array(src), dst)
+    cache_fork(c, ints(src), ints(dst))
+    cache_status(c)
+    same(c, m)
+    # pages that are not copies, and the tokens behind a copy's, are as they were
+    copies = {int(m.table[b, m.lengths[b] // chunk]): int(m.lengths[b] % chunk) for b in (5, 8, 6)}
+    for n, before in pools.items():
+        after = getattr(c, n).view(torch.uint8)
+        for p in range(40):
+            a = copies.get(p, 0)
+            assert torch.equal(after[p, :, a:], before[p, :, a:]), (n, p)
+    q = rng.standard_normal((9, 2 * heads, d))
+    check_decode(c, m, q, 0)
+    # parent and child go on apart
+    k, v = (bf16(rng.standard_normal((3, heads, d))) for _ in "kv")
+    new = [1, 0, 0, 0, 0, 1, 0, 0, 1]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    start = m.lengths.copy()
+    m.append(k.double().numpy(), v.double().numpy(), cu, start)
+    cache_append(c, k.cuda(), v.cuda(), ints(cu), ints(start))
+    cache_status(c)
+    same(c, m)
+
+
+def test_fork_is_all_or_nothing():
+    rng = np.random.default_rng(32)
+    c, m = pair(5, 6, 3, 1, 64, 128)
+    fill(c, m, rng, [200, 50, 0, 0, 0, 0])
+    cases = [([0, 0, 1], [2, 3, 4], moba.ERR_NO_PAGES),  # three copies, two free pages
+             ([0], [6], moba.ERR_INVALID_ARG), ([0], [-1], moba.ERR_INVALID_ARG), ([6], [2], moba.ERR_INVALID_ARG),
+             ([-1], [2], moba.ERR_INVALID_ARG), ([0], [0], moba.ERR_INVALID_ARG), ([0], [1], moba.ERR_INVALID_ARG),
+             ([0, 1], [2, 2], moba.ERR_INVALID_ARG), ([0, 1], [2, 2 ** 31 - 1], moba.ERR_INVALID_ARG)]
+    for src, dst, want in cases:
+        cache_fork(c, ints(src), ints(dst))
+        with pytest.raises(moba.MobaError) as e:
+            cache_status(c)
+        assert e.value.status == want, (src, dst)
+        same(c, m)
+    for entry in (5, -1, -7):  # a source whose table is broken
+        c.table[0, 0] = entry
+        cache_fork(c, ints([0]), ints([2]))
+        with pytest.raises(moba.MobaError):
+            cache_status(c)
+        c.table[0, 0] = int(m.table[0, 0])
+        same(c, m)
+
+
+def test_free_twice_and_unused():
+    rng = np.random.default_rng(33)
+    c, m = pair(10, 5, 4, 1, 64, 128)
+    fill(c, m, rng, [300, 128, 0, 0, 0])
+    m.fork(np.array([0]), [3])
+    cache_fork(c, ints([0]), ints([3]))
+    m.free([0, 4])
+    cache_free(c, ints([0, 4, 0, 0]))
+    cache_status(c)
+    same(c, m)
+    for bad in (5, -1, -2 ** 31):
+        cache_free(c, ints([bad]))
+        with pytest.raises(moba.MobaError):
+            cache_status(c)
+    m.free([3, 1])
+    cache_free(c, ints([3, 1]))
+    same(c, m)
+    assert not c.refs.any()
+    cache_free(c, ints([]))
+    cache_fork(c, ints([]), ints([]))
+
+
+@pytest.mark.parametrize("d,heads,chunk", [(64, 3, 128), (128, 1, 640)])
+def test_compact_packs_in_order(d, heads, chunk):
+    rng = np.random.default_rng(34)
+    c, m = pair(30, 6, 5, heads, d, chunk)
+    fill(c, m, rng, [3 * chunk, 70, 2 * chunk + 1, chunk - 1, 5, 0])
+    m.fork(np.array([2]), [5])
+    cache_fork(c, ints([2]), ints([5]))
+    m.free([0, 3])
+    cache_free(c, ints([0, 3]))
+    live = int((m.refs > 0).sum())
+    for pages in (live, live + 7, 60):
+        d2, m2 = pair(pages, 6, 5, heads, d, chunk)
+        d2.table.fill_(3)
+        d2.refs.fill_(9)
+        assert m.compact(m2)
+        tail = d2.k_codes[live:].clone()
+        cache_compact(c, d2)
+        cache_status(c)
+        same(d2, m2)
+        assert torch.equal(d2.k_codes[live:], tail)
+        q = rng.standard_normal((6, heads, d))
+        check_decode(d2, m2, q, 2)
+    small, _ = pair(live - 1, 6, 5, heads, d, chunk)
+    before = [t.view(torch.uint8).clone() for t in (small.k_codes, small.table, small.refs, small.lengths)]
+    cache_compact(c, small)
+    with pytest.raises(moba.MobaError) as e:
+        cache_status(c)
+    assert e.value.status == moba.ERR_NO_PAGES
+    for a, b in zip(before, (small.k_codes, small.table, small.refs, small.lengths)):
+        assert torch.equal(a, b.view(torch.uint8))
+    c.table[1, 4] = 29 if m.refs[29] == 0 else 10 ** 6  # an entry that names no page in use
+    d2, m2 = pair(60, 6, 5, heads, d, chunk)
+    cache_compact(c, d2)
+    with pytest.raises(moba.MobaError):
+        cache_status(c)
+    assert d2.table[1, 4] == -1
+
+
+# ---- together -----------------------------------------------------------------------------------
+
+def test_a_serving_run():
+    """Prompts, decode steps, forks, finished sequences and a smaller pool, as a server mixes them: the cache
+    is the model's after every step."""
+    rng = np.random.default_rng(40)
+    heads, group, d, chunk, seqs = 2, 2, 64, 128, 6
+    c, m = pair(40, seqs, 8, heads, d, chunk)
+    fill(c, m, rng, [400, 130, 0, 255, 0, 0])
+    for step in range(12):
+        new = (m.lengths > 0).astype(int)
+        if step == 4:  # a new prompt joins in a free slot
+            new[int(np.flatnonzero(m.lengths == 0)[0])] = 311
+        cu = np.concatenate([[0], np.cumsum(new)])
+        start = m.lengths.copy()
+        k, v = (bf16(rng.standard_normal((cu[-1], heads, d)) + 0.3 * step) for _ in "kv")
+        assert m.reserve(start + new)
+        m.append(k.double().numpy(), v.double().numpy(), cu, start)
+        cache_reserve(c, ints(start + new))
+        cache_append(c, k.cuda(), v.cuda(), ints(cu), ints(start))
+        check_decode(c, m, rng.standard_normal((seqs, heads * group, d)), (0, 2, 3)[step % 3])
+        if step in (2, 6, 9):  # the first sequence goes on twice
+            to = int(np.flatnonzero(m.lengths == 0)[0])
+            assert m.fork(np.array([0]), [to])
+            cache_fork(c, ints([0]), ints([to]))
+        if step in (5, 8):
+            gone = int(np.flatnonzero(m.lengths > 0)[-1])
+            m.free([gone])
+            cache_free(c, ints([gone]))
+        if step == 7:
+            c2, m2 = pair(30, seqs, 8, heads, d, chunk)
+            assert m.compact(m2)
+            cache_compact(c, c2)
+            cache_status(c)
+            c, m = c2, m2
+        cache_status(c)
+        same(c, m)
+
+
+def test_a_captured_step_replays():
+    """Reserve, append and decode of one token captured into a graph, replayed with other inputs, equal the
+    eager calls; two graphs with workspaces of their own run on two streams at once."""
+    rng = np.random.default_rng(41)
+    heads, d, chunk, seqs = 2, 128, 128, 4
+    k, v = (torch.tensor(rng.standard_normal((200, seqs, heads, d))).bfloat16().cuda() for _ in "kv")
+    qs = torch.tensor(rng.standard_normal((200, seqs, 2 * heads, d))).bfloat16().cuda()
+    cu, one = ints(range(seqs + 1)), torch.ones(seqs, dtype=torch.int32, device="cuda")
+
+    def step(c, kk, vv, q, start, upto, topk):
+        torch.add(start, one, out=upto)
+        cache_reserve(c, upto)
+        cache_append(c, kk, vv, cu, start)
+        r = cache_decode(c, q, topk)
+        start.copy_(upto)
+        return r
+
+    want = {}
+    for topk in (0, 2):
+        c = KVCache(16, seqs, 4, heads, d, chunk)
+        start, upto = ints([0] * seqs), ints([0] * seqs)
+        want[topk] = [[t.clone() for t in step(c, k[i], v[i], qs[i], start, upto, topk)] for i in range(200)]
+        cache_status(c)
+    runs = {}
+    for topk in (0, 2):
+        c = KVCache(16, seqs, 4, heads, d, chunk)
+        start, upto = ints([0] * seqs), ints([0] * seqs)
+        kk, vv, q = k[0].clone(), v[0].clone(), qs[0].clone()
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            step(c, kk, vv, q, start, upto, topk)
+            cache_free(c, ints(range(seqs)))
+            start.zero_()
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = step(c, kk, vv, q, start, upto, topk)
+        runs[topk] = (c, g, s, (kk, vv, q), got, start, upto)  # a graph's tensors live as long as it does
+    torch.cuda.synchronize()
+    for i in range(200):
+        for topk, (c, g, s, ins, got, *_) in runs.items():
+            with torch.cuda.stream(s):
+                for a, b in zip(ins, (k[i], v[i], qs[i])):
+                    a.copy_(b)
+                g.replay()
+        for topk, (c, g, s, ins, got, *_) in runs.items():
+            s.synchronize()
+            for a, b in zip(got, want[topk][i]):
+                assert torch.equal(a, b), (topk, i)
+    for c, *_ in runs.values():
+        cache_status(c)
+
+
+def test_calls_repeat_and_take_buffers():
+    """Repeated calls give the same bits; a caller's workspace (with any contents), out and lse are used."""
+    rng = np.random.default_rng(42)
+    c, m = pair(60, 5, 12, 2, 128, 128)
+    fill(c, m, rng, [1500, 129, 0, 1000, 700])
+    q = bf16(rng.standard_normal((5, 8, 128))).cuda()
+    for topk in (0, 1, 4):
+        o, l = cache_decode(c, q, topk)
+        n = c._lib.moba_cache_decode_workspace_size(c._ref, 8, topk)
+        for byte in (0, 0xff, 0x7f):
+            ws = torch.full((n,), byte, dtype=torch.uint8, device="cuda")
+            out, lse = torch.empty_like(o), torch.empty_like(l)
+            r = cache_decode(c, q, topk, workspace=ws, out=out, lse=lse)
+            assert r[0] is out and r[1] is lse
+            assert torch.equal(out, o) and torch.equal(lse, l)
+    with pytest.raises(moba.MobaError):
+        cache_decode(c, q, 4, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    cache_status(c)
+
+
+def test_binding_refuses_what_does_not_fit():
+    c = KVCache(4, 2, 2, 2, 64, 128)
+    x = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16, device="cuda")
+    bad = [lambda: cache_append(c, x, x[:2], ints([0, 1, 3]), ints([0, 0])),
+           lambda: cache_append(c, x.float(), x, ints([0, 1, 3]), ints([0, 0])),
+           lambda: cache_append(c, x.transpose(0, 1).contiguous().transpose(0, 1), x, ints([0, 1, 3]), ints([0, 0])),
+           lambda: cache_append(c, x, x, ints([0, 3]), ints([0, 0])),
+           lambda: cache_append(c, x, x, ints([0, 1, 3]).long(), ints([0, 0])),
+           lambda: cache_append(c, x, x, ints([0, 1, 3]), ints([0, 0]).cpu()),
+           lambda: cache_decode(c, q[:1], 1), lambda: cache_decode(c, q.half(), 1), lambda: cache_decode(c, q[0], 1),
+           lambda: cache_decode(c, q, 1, out=q[:1]), lambda: cache_decode(c, q, 1, lse=torch.zeros(2, 2, device="cuda")),
+           lambda: cache_decode(c, q, 1, workspace=torch.zeros(1 << 20, dtype=torch.uint8)),
+           lambda: cache_fork(c, ints([0]), ints([1, 1])), lambda: cache_fork(c, ints([0]).long(), ints([1])),
+           lambda: cache_free(c, ints([0]).cpu()), lambda: cache_reserve(c, ints([1])),
+           lambda: KVCache.from_tensors(c.k_codes, c.k_scales.view(torch.uint8), c.v_codes, c.v_scales, c.k_mean, c.refs,
+                                        c.table, c.lengths),
+           lambda: KVCache.from_tensors(c.k_codes, c.k_scales, c.v_codes[:2], c.v_scales, c.k_mean, c.refs, c.table,
+                                        c.lengths)]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"case {i} accepted")
+    for hq, topk in ((3, 1), (4, 33), (4, -1)):
+        with pytest.raises(moba.MobaError):
+            cache_decode(c, torch.zeros((2, hq, 64), dtype=torch.bfloat16, device="cuda"), topk)
+    with pytest.raises(moba.MobaError):
+        cache_compact(c, c)
+    with pytest.raises(moba.MobaError):
+        KVCache(4, 2, 2, 2, 64, 100)
+    cache_status(c)
