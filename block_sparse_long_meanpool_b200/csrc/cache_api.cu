@@ -110,11 +110,18 @@ cache::View view(const moba_cache& c) {
     return v;
 }
 
+int device_sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+    return n;
+}
+
 size_t page_ws_bytes(const moba_cache& c) { return 4 * cache::page_ws_words(c.num_pages, c.num_seqs); }
 
 struct DecodeLayout {
     int hgroups, rows, max_items;
-    size_t items, counts, total;
+    size_t items, tiles, done, part_o, part_ml, total;
 };
 
 // Shapes of a decode call; MOBA_OK with the layout in *L.
@@ -135,8 +142,11 @@ moba_status decode_layout(const moba_cache* c, int hq, int topk, DecodeLayout* L
     const int most = (group < cache::kRowHeads ? group : cache::kRowHeads) * (topk - 1) + 1;
     L->max_items = topk == 0 ? 0 : most < c->max_blocks ? most : c->max_blocks;
     L->items = 0;
-    L->counts = align_up(sizeof(int2) * (size_t)L->rows * L->max_items);
-    L->total = L->counts + align_up(4ull * L->rows);
+    L->tiles = align_up(sizeof(int2) * (size_t)L->rows * L->max_items);
+    L->done = L->tiles + align_up(4ull * L->rows);
+    L->part_o = L->done + align_up(4ull * L->rows);
+    L->part_ml = L->part_o + align_up(4ull * 2 * cache::kMaxCtas * cache::kRowHeads * c->head_dim);
+    L->total = L->part_ml + align_up(sizeof(float2) * 2 * cache::kMaxCtas * cache::kRowHeads);
     return MOBA_OK;
 }
 
@@ -221,8 +231,11 @@ moba_status moba_cache_decode(const moba_cache* c, const void* q, int num_q_head
     cache::DecodeWs ws;
     char* base = static_cast<char*>(workspace);
     ws.items = reinterpret_cast<int2*>(base + L.items);
-    ws.counts = reinterpret_cast<int*>(base + L.counts);
-    const cudaError_t e = cache::launch_decode(view(*c), a, ws, static_cast<cudaStream_t>(stream));
+    ws.tiles = reinterpret_cast<int*>(base + L.tiles);
+    ws.done = reinterpret_cast<int*>(base + L.done);
+    ws.part_o = reinterpret_cast<float*>(base + L.part_o);
+    ws.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
+    const cudaError_t e = cache::launch_decode(view(*c), a, ws, device_sm_count(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOBA_OK : cuda_fail(e, "cache decode launch");
 }
 

@@ -6,11 +6,13 @@
 // keys and values.  The query heads of a KV head are taken together, up to kRowHeads at a time (a
 // "row"), so that a block that several of them attend to is read once.
 //   cache_plan_kernel  one CTA per row: gate scores, the heads' choices, their union
-//   cache_attn_kernel  one CTA per row: online softmax over the row's blocks
+//   cache_attn_kernel  as many CTAs as fit the GPU at once, each with an equal share of all rows'
+//                      64-token tiles; a row that several CTAs share is merged by the last of them
 #include <climits>
 
 #include "cache_internal.cuh"
 #include "moba_internal.cuh"
+#include "ptx.cuh"
 
 namespace moba {
 namespace cache {
@@ -41,8 +43,9 @@ __device__ __forceinline__ int held_tokens(const View& c, int seq) {
     return L < 0 || L > (long long)c.max_blocks * c.chunk ? 0 : L;
 }
 
-// items[row] lists the row's blocks ascending, the own block last, as (page, heads that attend);
-// counts[row] is their number (0: an empty sequence, whose outputs are written here).
+// items[row] lists the row's blocks ascending, the own block last, as (page, heads that attend)
+// (not written for topk = 0: the row's blocks are the table's); tiles[row] is the number of its
+// tiles, 0 for an empty sequence, whose outputs are written here.
 template <int D, int K>
 __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs a, DecodeWs ws) {
     constexpr int V = D / 32;
@@ -54,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs
     const int L = held_tokens(c, w.seq);
     if (L == 0) {
         if (tid == 0) {
-            ws.counts[r] = 0;
+            ws.tiles[r] = 0;
             if (__ldg(c.lengths + w.seq) != 0) report(c, MOBA_ERR_INVALID_ARG);
         }
         for (int i = tid; i < w.nh * D; i += kThreads)
@@ -66,9 +69,11 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs
     const int* row = c.table + (size_t)w.seq * c.max_blocks;
     int2* items = ws.items + (size_t)r * a.max_items;
     const int all = (1 << w.nh) - 1;
+    const int own_tiles = (L - own * c.chunk + kTile - 1) / kTile, per_block = c.chunk / kTile;
+    if (tid == 0) ws.done[r] = 0;
     const int n_route = min(a.topk - 1, own);
     if (a.topk == 0 || n_route == own) {  // every block
-        if (tid == 0) ws.counts[r] = own + 1;
+        if (tid == 0) ws.tiles[r] = own * per_block + own_tiles;
         if (a.topk)
             for (int j = tid; j <= own; j += kThreads) items[j] = make_int2(__ldg(row + j), all);
         return;
@@ -163,121 +168,468 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs
     const int leaders = __syncthreads_count(mine >= 0);
     if (tid == 0) {
         items[leaders] = make_int2(__ldg(row + own), all);
-        ws.counts[r] = leaders + 1;
+        ws.tiles[r] = leaders * per_block + own_tiles;
     }
 }
 
-// Held values of one tile (rows [t0, t0 + n) of a page) into xs[kTile][D + 1], fp32.
+// ---- attention ----------------------------------------------------------------------------
+//
+// A warp takes whole tiles of 64 tokens.  Codes and scales come by bulk copies into a ring of its
+// own; e2m1 -> fp16 conversion and the scale's product are exact, so the tensor cores (mma.sync
+// m16n8k16, fp16 operands, fp32 sums) see the held values themselves:
+//   S^T [keys x heads] = K [keys x d] q^T      K's fragments straight from its rows: the thread
+//                                              that owns key g, quarter t of the channels loads one
+//                                              vector; the order of the channels is free as long
+//                                              as q's fragments follow it
+//   O^T [d x heads] += V^T [d x keys] P^T      P^T's fragments are S^T's through movmatrix; V^T
+//                                              needs pairs of keys of one channel, formed by
+//                                              interleaving the nibbles of two rows before the
+//                                              conversion (2 operations per 8 codes)
+// One query per head makes N = 8 columns (heads) of each product; tcgen05 would want 128 rows of M
+// and its operands written to shared memory, and the tensor pipe is not what bounds this kernel.
+// q is scaled by a power of two per head so that its largest channel is in [2^14, 2^15): fp16 then
+// holds every channel down to 2^-28 of the largest one exactly, and the rest to 2^-39 of it.
+// p <= 1 is rounded to fp16 (2^-11 relative, an eighth of the bf16 output's own rounding; below
+// 2^-14 an absolute 2^-25, against a sum of at least 1); the sum l is taken before that rounding.
+
+constexpr int kWarps = 8;
+constexpr int kStages = 2;
+
 template <int D>
-__device__ __forceinline__ void load_tile(const uint8_t* codes, const uint8_t* scales, int n, float* xs) {
-    constexpr int kPerTok = D / kGroup;
-    for (int i = threadIdx.x; i < n * kPerTok; i += kThreads) {
-        const int t = i / kPerTok, grp = i - t * kPerTok;
-        const uint2 w = *reinterpret_cast<const uint2*>(codes + (size_t)t * (D / 2) + grp * 8);
-        const float s = f16x2_to_f32(e4m3x2_to_f16x2(scales[(size_t)t * kPerTok + grp])).x;
-        uint32_t h[4];
-        float* x = xs + t * (D + 1) + grp * kGroup;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            e2m1x8_to_f16x2(k ? w.y : w.x, h);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = f16x2_to_f32(h[j]);
-                x[8 * k + 2 * j] = f.x * s;
-                x[8 * k + 2 * j + 1] = f.y * s;
-            }
-        }
-    }
+struct Tile {
+    static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / kGroup;
+    static constexpr int kK = 0, kKs = kCodes, kV = kKs + kScales, kVs = kV + kCodes;
+    static constexpr int kBytes = 2 * (kCodes + kScales);
+};
+template <int D>
+struct Smem {
+    static constexpr int kRing = 0;
+    static constexpr int kState = kRing + kWarps * kStages * Tile<D>::kBytes;  // [warps][heads][D] fp32
+    static constexpr int kMl = kState + kWarps * kRowHeads * D * 4;  // [warps][heads] float2
+    static constexpr int kMeta = kMl + kWarps * kRowHeads * 8;       // [warps][stages] int2
+    static constexpr int kBars = kMeta + kWarps * kStages * 8;
+    static constexpr int kMisc = kBars + kWarps * kStages * 8;  // scan and flags
+    static constexpr int kTotal = kMisc + 256;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int N>
+__device__ __forceinline__ void lds(uint32_t (&w)[N], uint32_t addr) {
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(addr));
+    else if constexpr (N == 2)
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    else
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+    uint32_t x;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr));
+    return x;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+    uint32_t x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(addr));
+    return x;
+}
+
+// The tiles of a CTA: [begin, end) of all rows' tiles in order.  A segment is the part of a row
+// within it.
+struct Segment {
+    int row, at, t0, n;  // row; first tile as counted from begin; as counted in the row; tiles
+};
+__device__ __forceinline__ void next_segment(Segment& s, const int* __restrict__ tiles, int total) {
+    s.at += s.n;
+    s.t0 = 0;
+    do s.n = __ldcg(tiles + ++s.row);
+    while (s.n == 0);
+    s.n = min(s.n, total - s.at);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) cache_attn_kernel(View c, DecodeArgs a, DecodeWs ws) {
-    constexpr int kSub = kThreads / D, kPer = kRowHeads / kSub;  // heads per thread of the value product
-    __shared__ float qs[kRowHeads][D];
-    __shared__ float xs[kTile * (D + 1)];
-    __shared__ float ps[kRowHeads][kTile];
-    __shared__ float alpha[kRowHeads];
-    const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Row w = row_of(c, a, r);
-    const int items = ws.counts[r];
-    if (items == 0) return;
-    const int L = held_tokens(c, w.seq), own = (L - 1) / c.chunk;
-    for (int i = tid; i < kRowHeads * D; i += kThreads) {
-        const int h = i / D;
-        qs[h][i - h * D] =
-            h < w.nh ? __bfloat162float(a.q[((size_t)w.seq * a.hq + w.h0) * D + i]) * a.scale_log2 : 0.f;
-    }
-    float m = -INFINITY, l = 0.f;  // of head `warp`
-    float acc[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-    const int dim = tid % D, sub = tid / D;
-    for (int it = 0; it < items; ++it) {
-        const int2 item = a.topk ? ws.items[(size_t)r * a.max_items + it]
-                                 : make_int2(__ldg(c.table + (size_t)w.seq * c.max_blocks + it), (1 << w.nh) - 1);
-        const int tokens = it == items - 1 ? L - own * c.chunk : c.chunk;
-        if (item.x < 0 || item.x >= c.pages) {
-            if (tid == 0) report(c, MOBA_ERR_INVALID_ARG);
-            continue;
-        }
-        const size_t cr = code_row(c, item.x, w.g), sr = scale_row(c, item.x, w.g);
-        for (int t0 = 0; t0 < tokens; t0 += kTile) {
-            const int n = min(kTile, tokens - t0);
-            const size_t co = cr + (size_t)t0 * (D / 2), so = sr + (size_t)t0 * (D / kGroup);
-            __syncthreads();
-            load_tile<D>(c.kc + co, c.ks + so, n, xs);
-            __syncthreads();
-            for (int i = tid; i < kRowHeads * kTile; i += kThreads) {
-                const int key = i % kTile, h = i / kTile;
-                float s = 0.f;
-                for (int e = 0; e < D; ++e) s = fmaf(qs[h][e], xs[key * (D + 1) + e], s);
-                ps[h][key] = key < n && (item.y >> h & 1) ? s : -INFINITY;
-            }
-            __syncthreads();
-            load_tile<D>(c.vc + co, c.vs + so, n, xs);
-            {
-                const float x = ps[warp][lane], y = ps[warp][lane + 32];
-                float top = fmaxf(x, y);
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-                const float al = exp2f(m - ref), px = exp2f(x - ref), py = exp2f(y - ref);
-                float ts = px + py;
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) ts += __shfl_xor_sync(0xffffffffu, ts, off);
-                ps[warp][lane] = px;
-                ps[warp][lane + 32] = py;
-                l = l * al + ts;
-                m = mn;
-                if (lane == 0) alpha[warp] = al;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int h = sub * kPer + i;
-                float o = acc[i] * alpha[h];
-                for (int k = 0; k < n; ++k) o = fmaf(ps[h][k], xs[k * (D + 1) + dim], o);
-                acc[i] = o;
-            }
-        }
-    }
-    __syncthreads();
+__global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, DecodeArgs a, DecodeWs ws) {
+    using T = Tile<D>;
+    using S = Smem<D>;
+    constexpr int kMt = D / 16;      // 16-channel tiles of O^T; 16-channel steps of K q
+    constexpr int kKw = D / 32;      // 32-bit words of a thread's quarter of a key's codes
+    constexpr int kVw = D / 64;      // words of a thread's eighth of a value's codes
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+    const uint32_t base = ptx::smem_u32(smem);
+    volatile int* abort_flag = reinterpret_cast<int*>(smem + S::kMisc);
+    long long* scan = reinterpret_cast<long long*>(smem + S::kMisc + 8);  // warp sums, then (first row, its start)
+    const uint32_t bars = base + S::kBars + warp * kStages * 8;
     if (lane == 0) {
-        ps[0][warp] = l > 0.f ? c.v_unit / l : l == 0.f ? 0.f : l;
-        if (warp < w.nh)
-            a.lse[(size_t)(w.h0 + warp) * c.seqs + w.seq] = m * 0.69314718055994531f + logf(l);
+        for (int i = 0; i < kStages; ++i) ptx::mbar_init(bars + 8 * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tid == 0) *abort_flag = 0;
+
+    // Every CTA adds up the rows' tiles: thread i takes a contiguous part of the rows.
+    const int per_thread = (a.rows + kWarps * 32 - 1) / (kWarps * 32);
+    const int r0 = min(a.rows, tid * per_thread), r1 = min(a.rows, r0 + per_thread);
+    long long mine = 0;
+    for (int r = r0; r < r1; ++r) mine += __ldcg(ws.tiles + r);
+    long long incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine, all_tiles = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += scan[i];
+        all_tiles += scan[i];
+    }
+    // CTAs that work: at least one tile for each warp where there are that few
+    const long long ctas = max(1LL, min((long long)gridDim.x, (all_tiles + kWarps - 1) / kWarps));
+    const long long begin = blockIdx.x * all_tiles / ctas, end = (blockIdx.x + 1) * all_tiles / ctas;
+    if (blockIdx.x >= ctas || begin >= end) return;
+    __syncthreads();
+    if (before <= begin && begin < before + mine) {
+        long long at = before;
+        int r = r0;
+        for (int n; at + (n = __ldcg(ws.tiles + r)) <= begin; ++r) at += n;
+        scan[kWarps] = r;
+        scan[kWarps + 1] = at;
     }
     __syncthreads();
+    const int total = (int)(end - begin);
+    Segment seg;
+    seg.row = (int)scan[kWarps];
+    long long row_start = scan[kWarps + 1];  // first tile of seg's row among all tiles
+    seg.at = 0;
+    seg.t0 = (int)(begin - row_start);
+    seg.n = min(__ldcg(ws.tiles + seg.row) - seg.t0, total);
+
+    // The copies run ahead of the products on a cursor of their own.
+    const int per_block = c.chunk / kTile;
+    Segment ahead = seg;
+    Row arow = row_of(c, a, ahead.row);
+    int alen = held_tokens(c, arow.seq);
+    int issued = 0;
+    bool alive = true;
+    auto issue = [&]() {
+        const int i = warp + issued * kWarps;
+        if (i >= total || !alive) return;
+        if (i >= ahead.at + ahead.n) {
+            do next_segment(ahead, ws.tiles, total);
+            while (i >= ahead.at + ahead.n);
+            arow = row_of(c, a, ahead.row);
+            alen = held_tokens(c, arow.seq);
+        }
+        const int tile = ahead.t0 + i - ahead.at, item = tile / per_block, sub = tile - item * per_block;
+        int2 it = make_int2(0, (1 << arow.nh) - 1);
+        if (a.topk)
+            it = __ldcg(ws.items + (size_t)ahead.row * a.max_items + item);
+        else
+            it.x = __ldg(c.table + (size_t)arow.seq * c.max_blocks + item);
+        const int last = (alen - 1) % c.chunk + 1 - sub * kTile;  // tokens left in an own block's tile
+        const bool own = ahead.t0 + i - ahead.at >= __ldcg(ws.tiles + ahead.row) - ((alen - 1) % c.chunk / kTile + 1);
+        int valid = own ? min(kTile, last) : kTile;
+        const int stage = issued % kStages;
+        const uint32_t dst = base + S::kRing + (warp * kStages + stage) * T::kBytes, bar = bars + 8 * stage;
+        if (it.x < 0 || it.x >= c.pages) valid = 0;
+        if (lane == 0) {
+            *reinterpret_cast<int2*>(smem + S::kMeta + (warp * kStages + stage) * 8) = make_int2(valid, it.y);
+            if (valid) {
+                const size_t cr = code_row(c, it.x, arow.g) + (size_t)sub * T::kCodes;
+                const size_t sr = scale_row(c, it.x, arow.g) + (size_t)sub * T::kScales;
+                ptx::mbar_arrive_tx(bar, T::kBytes);
+                bulk_load(dst + T::kK, c.kc + cr, T::kCodes, bar);
+                bulk_load(dst + T::kKs, c.ks + sr, T::kScales, bar);
+                bulk_load(dst + T::kV, c.vc + cr, T::kCodes, bar);
+                bulk_load(dst + T::kVs, c.vs + sr, T::kScales, bar);
+            } else {
+                ptx::mbar_arrive(bar);
+                report(c, MOBA_ERR_INVALID_ARG);
+            }
+        }
+        ++issued;
+    };
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int h = sub * kPer + i;
-        if (h < w.nh)
-            a.out[((size_t)w.seq * a.hq + w.h0 + h) * D + dim] = __float2bfloat16_rn(acc[i] * ps[0][h]);
+    for (int i = 0; i < kStages; ++i) issue();
+
+    float* state = reinterpret_cast<float*>(smem + S::kState);
+    float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
+    int used = 0;  // tiles this warp has taken
+    for (;;) {
+        const Row w = row_of(c, a, seg.row);
+        // q's fragments: head g8, channels t4 * (D / 4) ..
+        uint32_t qf[D / 8];
+        float unit;
+        {
+            uint32_t raw[D / 8];
+            const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)w.seq * a.hq + w.h0 + g8) * D + t4 * (D / 4));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 x = g8 < w.nh ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                raw[4 * i] = x.x;
+                raw[4 * i + 1] = x.y;
+                raw[4 * i + 2] = x.z;
+                raw[4 * i + 3] = x.w;
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, raw[i] & 0x7fff7fffu);
+            top = max(top & 0xffffu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^(14 - e) for a largest magnitude in [2^e, 2^(e+1)), within fp32's normal range
+            const int fb = min(268 - (int)(top >> 7), 253);
+            const float f = __uint_as_float((uint32_t)fb << 23);
+            unit = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)(254 - fb) << 23), 1e-37f);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                qf[i] = pack_f16(__uint_as_float(raw[i] << 16) * f, __uint_as_float(raw[i] & 0xffff0000u) * f);
+        }
+        // this thread's columns of S^T and O^T are heads 2 t4 and 2 t4 + 1
+        const float unit0 = __shfl_sync(0xffffffffu, unit, 8 * t4), unit1 = __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        float o[kMt][4];
+#pragma unroll
+        for (int i = 0; i < kMt; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+        for (; warp + used * kWarps < seg.at + seg.n; ++used) {
+            const int stage = used % kStages;
+            const uint32_t src = base + S::kRing + (warp * kStages + stage) * T::kBytes;
+            if (alive) alive = ptx::wait_bar(bars + 8 * stage, used / kStages & 1, abort_flag, c.status);
+            const int2 meta = *reinterpret_cast<const int2*>(smem + S::kMeta + (warp * kStages + stage) * 8);
+            if (alive && meta.x) {
+                const int valid = meta.x;
+                const bool on0 = meta.y >> (2 * t4) & 1, on1 = meta.y >> (2 * t4 + 1) & 1;
+                // Rows of the 8-row groups are taken in the order 0 1 2 3 5 4 7 6: the rows that
+                // one load reads, by g8 for K and by t4 for V, then fall into different banks.
+                const int kr = g8 ^ (g8 >> 2), va = (2 * t4) ^ (t4 >> 1), vb = (2 * t4 + 1) ^ (t4 >> 1);
+                float s[kTile / 16][4];
+#pragma unroll
+                for (int mt = 0; mt < kTile / 16; ++mt) {
+                    s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
+                    uint32_t x[2][kKw], sc[2][2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = mt * 16 + 8 * h + kr;
+                        lds<kKw>(x[h], src + T::kK + key * (D / 2) + t4 * (D / 8));
+                        if constexpr (D == 128) {
+                            const uint32_t two = e4m3x2_to_f16x2(lds_u16(src + T::kKs + key * 8 + 2 * t4));
+                            sc[h][0] = __byte_perm(two, 0, 0x1010);
+                            sc[h][1] = __byte_perm(two, 0, 0x3232);
+                        } else {
+                            const uint32_t one = lds_u8(src + T::kKs + key * 4 + t4);
+                            sc[h][0] = sc[h][1] = e4m3x2_to_f16x2(one | one << 8);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kKw; ++i) {
+                        uint32_t lo[4], hi[4];
+                        e2m1x8_to_f16x2(x[0][i], lo);
+                        e2m1x8_to_f16x2(x[1][i], hi);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            lo[j] = hmul2(lo[j], sc[0][i / 2]);
+                            hi[j] = hmul2(hi[j], sc[1][i / 2]);
+                        }
+                        mma16816(s[mt], lo[0], hi[0], lo[1], hi[1], qf[4 * i], qf[4 * i + 1]);
+                        mma16816(s[mt], lo[2], hi[2], lo[3], hi[3], qf[4 * i + 2], qf[4 * i + 3]);
+                    }
+                }
+                float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+                for (int mt = 0; mt < kTile / 16; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bool ok = mt * 16 + 8 * h + kr < valid;
+                        s[mt][2 * h] = ok && on0 ? s[mt][2 * h] : -INFINITY;
+                        s[mt][2 * h + 1] = ok && on1 ? s[mt][2 * h + 1] : -INFINITY;
+                        x0 = fmaxf(x0, s[mt][2 * h]);
+                        x1 = fmaxf(x1, s[mt][2 * h + 1]);
+                    }
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+                }
+                const float n0 = fmaxf(m0, x0 * unit0), n1 = fmaxf(m1, x1 * unit1);
+                const float ref0 = n0 == -INFINITY ? 0.f : n0, ref1 = n1 == -INFINITY ? 0.f : n1;
+                const float al0 = ptx::ex2(m0 - ref0), al1 = ptx::ex2(m1 - ref1);
+                m0 = n0;
+                m1 = n1;
+                if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
+                    l0 *= al0;
+                    l1 *= al1;
+#pragma unroll
+                    for (int i = 0; i < kMt; ++i) {
+                        o[i][0] *= al0;
+                        o[i][1] *= al1;
+                        o[i][2] *= al0;
+                        o[i][3] *= al1;
+                    }
+                }
+                uint32_t p[kTile / 16][2];
+#pragma unroll
+                for (int mt = 0; mt < kTile / 16; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float p0 = ptx::ex2(fmaf(s[mt][2 * h], unit0, -ref0));
+                        const float p1 = ptx::ex2(fmaf(s[mt][2 * h + 1], unit1, -ref1));
+                        l0 += p0;
+                        l1 += p1;
+                        p[mt][h] = transpose8x8(pack_f16(p0, p1));
+                    }
+#pragma unroll
+                for (int mt = 0; mt < kTile / 16; ++mt) {
+                    // keys va, vb of the step's rows 0..7 and of its rows 8..15
+                    uint32_t x[4][kVw], sc[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int ka = mt * 16 + 8 * h + va, kb = mt * 16 + 8 * h + vb;
+                        lds<kVw>(x[2 * h], src + T::kV + ka * (D / 2) + g8 * (D / 16));
+                        lds<kVw>(x[2 * h + 1], src + T::kV + kb * (D / 2) + g8 * (D / 16));
+                        const int group = D == 128 ? g8 : g8 >> 1;
+                        uint32_t sa = lds_u8(src + T::kVs + ka * (D / kGroup) + group);
+                        uint32_t sb = lds_u8(src + T::kVs + kb * (D / kGroup) + group);
+                        sa = ka < valid ? sa : 0;  // what lies behind the last token may be anything
+                        sb = kb < valid ? sb : 0;
+                        sc[h] = e4m3x2_to_f16x2(sa | sb << 8);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kVw; ++i) {
+                        uint32_t e[2][4], f[2][4];  // even and odd channels, by rows' half
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t ra = x[2 * h][i], rb = x[2 * h + 1][i];
+                            e2m1x8_to_f16x2((ra & 0x0f0f0f0fu) | (rb << 4 & 0xf0f0f0f0u), e[h]);
+                            e2m1x8_to_f16x2((ra >> 4 & 0x0f0f0f0fu) | (rb & 0xf0f0f0f0u), f[h]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                e[h][j] = hmul2(e[h][j], sc[h]);
+                                f[h][j] = hmul2(f[h][j], sc[h]);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma16816(o[4 * i + j], e[0][j], f[0][j], e[1][j], f[1][j], p[mt][0], p[mt][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            issue();
+        }
+
+        // The warps' parts of the segment, then the CTA's.
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+        }
+        if (g8 == 0) {
+            ml[warp * kRowHeads + 2 * t4] = make_float2(m0, l0);
+            ml[warp * kRowHeads + 2 * t4 + 1] = make_float2(m1, l1);
+        }
+        float* mine_o = state + (warp * kRowHeads + 2 * t4) * D + g8 * (D / 8);
+#pragma unroll
+        for (int i = 0; i < kMt; ++i) {
+            *reinterpret_cast<float2*>(mine_o + 2 * i) = make_float2(o[i][0], o[i][2]);
+            *reinterpret_cast<float2*>(mine_o + D + 2 * i) = make_float2(o[i][1], o[i][3]);
+        }
+        __syncthreads();
+        const bool whole = seg.t0 == 0 && seg.n == __ldcg(ws.tiles + seg.row);
+        const int slot = 2 * blockIdx.x + (seg.at > 0);
+        for (int i = tid; i < w.nh * D; i += kWarps * 32) {
+            const int h = i / D, e = i - h * D;
+            float m = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) m = fmaxf(m, ml[k * kRowHeads + h].x);
+            const float ref = m == -INFINITY ? 0.f : m;
+            float l = 0.f, acc = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float2 x = ml[k * kRowHeads + h];
+                const float f = ptx::ex2(x.x - ref);
+                l = fmaf(f, x.y, l);
+                acc = fmaf(f, state[(k * kRowHeads + h) * D + e], acc);
+            }
+            if (whole) {
+                a.out[((size_t)w.seq * a.hq + w.h0 + h) * D + e] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l * c.v_unit);
+                if (e == 0) a.lse[(size_t)(w.h0 + h) * c.seqs + w.seq] = m * 0.69314718055994531f + logf(l);
+            } else {
+                ws.part_o[((size_t)slot * kRowHeads + h) * D + e] = acc;
+                if (e == 0) ws.part_ml[slot * kRowHeads + h] = make_float2(m, l);
+            }
+        }
+        if (!whole) {
+            // parts come from the CTAs that hold the row's first to last tile
+            const int n_row = __ldcg(ws.tiles + seg.row);
+            const int c0 = (int)(((row_start + 1) * ctas - 1) / all_tiles);
+            const int c1 = (int)(((row_start + n_row) * ctas - 1) / all_tiles);
+            int* last = reinterpret_cast<int*>(smem + S::kMisc + 4);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) *last = atomicAdd(ws.done + seg.row, 1) == c1 - c0;
+            __syncthreads();
+            if (*last) {
+                __threadfence();
+                for (int i = tid; i < w.nh * D; i += kWarps * 32) {
+                    const int h = i / D, e = i - h * D;
+                    float m = -INFINITY;
+                    for (int k = c0; k <= c1; ++k) {
+                        const int sl = 2 * k + (row_start > k * all_tiles / ctas);
+                        m = fmaxf(m, __ldcg(ws.part_ml + sl * kRowHeads + h).x);
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    float l = 0.f, acc = 0.f;
+                    for (int k = c0; k <= c1; ++k) {
+                        const int sl = 2 * k + (row_start > k * all_tiles / ctas);
+                        const float2 x = __ldcg(ws.part_ml + sl * kRowHeads + h);
+                        const float f = ptx::ex2(x.x - ref);
+                        l = fmaf(f, x.y, l);
+                        acc = fmaf(f, __ldcg(ws.part_o + ((size_t)sl * kRowHeads + h) * D + e), acc);
+                    }
+                    a.out[((size_t)w.seq * a.hq + w.h0 + h) * D + e] =
+                        __float2bfloat16_rn(l == 0.f ? 0.f : acc / l * c.v_unit);
+                    if (e == 0) a.lse[(size_t)(w.h0 + h) * c.seqs + w.seq] = m * 0.69314718055994531f + logf(l);
+                }
+            }
+        }
+        if (seg.at + seg.n >= total) break;
+        row_start += seg.t0 + seg.n;  // a segment that another follows ends its row
+        next_segment(seg, ws.tiles, total);
+        __syncthreads();  // the state is free again
     }
+    // after a wait that gave up: the copies still in flight land before the memory is given back
+    if (!alive)
+        for (int k = used > kStages ? issued - kStages : 0; k < issued; ++k)
+            ptx::drain_bar(bars + 8 * (k % kStages), k / kStages & 1);
 }
 
 template <int D>
-cudaError_t launch_decode_d(const View& c, const DecodeArgs& a, const DecodeWs& ws, cudaStream_t st) {
+cudaError_t launch_decode_d(const View& c, const DecodeArgs& a, const DecodeWs& ws, int num_sms, cudaStream_t st) {
     const int route = a.topk - 1;
     if (route <= 4)
         cache_plan_kernel<D, 4><<<a.rows, kThreads, 0, st>>>(c, a, ws);
@@ -289,14 +641,16 @@ cudaError_t launch_decode_d(const View& c, const DecodeArgs& a, const DecodeWs& 
         cache_plan_kernel<D, 32><<<a.rows, kThreads, 0, st>>>(c, a, ws);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cache_attn_kernel<D><<<a.rows, kThreads, 0, st>>>(c, a, ws);
+    e = cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+    if (e != cudaSuccess) return e;
+    cache_attn_kernel<D><<<min(num_sms, kMaxCtas), kWarps * 32, Smem<D>::kTotal, st>>>(c, a, ws);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_decode(const View& c, const DecodeArgs& a, const DecodeWs& ws, cudaStream_t st) {
-    return c.d == 64 ? launch_decode_d<64>(c, a, ws, st) : launch_decode_d<128>(c, a, ws, st);
+cudaError_t launch_decode(const View& c, const DecodeArgs& a, const DecodeWs& ws, int num_sms, cudaStream_t st) {
+    return c.d == 64 ? launch_decode_d<64>(c, a, ws, num_sms, st) : launch_decode_d<128>(c, a, ws, num_sms, st);
 }
 
 }  // namespace cache

@@ -113,11 +113,16 @@ struct DecodeArgs {
     __nv_bfloat16* out;
     float* lse;
 };
+// CTAs of the attention kernel at most (it runs as many as the device holds at once).
+constexpr int kMaxCtas = 296;
 struct DecodeWs {
-    int2* items;   // [rows, max_items]: (block, heads that attend to it), ascending blocks
-    int* counts;   // [rows]: items of each row
+    int2* items;     // [rows, max_items]: (page, heads that attend to it), ascending blocks
+    int* tiles;      // [rows]: tiles of each row
+    int* done;       // [rows]: CTAs that have written their part of the row
+    float* part_o;   // [2 * kMaxCtas, kRowHeads, d]: unnormalised outputs of a row's part
+    float2* part_ml;  // [2 * kMaxCtas, kRowHeads]: its running maximum (log2 units) and sum
 };
-cudaError_t launch_decode(const View& c, const DecodeArgs& a, const DecodeWs& ws, cudaStream_t st);
+cudaError_t launch_decode(const View& c, const DecodeArgs& a, const DecodeWs& ws, int num_sms, cudaStream_t st);
 
 }  // namespace cache
 }  // namespace moba

@@ -357,9 +357,10 @@ def test_decode_reports_bad_pages_and_lengths():
             o, l = cache_decode(c, q.cuda(), topk)
             with pytest.raises(moba.MobaError):
                 cache_status(c)
-            assert not o[1].any() and torch.isneginf(l[:, 1]).all()
-            assert torch.equal(o[::2], good[0][::2]) and torch.equal(l[:, ::2], good[1][:, ::2])
-            c.lengths[1] = 700
+            # fewer tokens in all are cut at other places, so the other rows' last bits may differ: the model's bounds
+            m.lengths[1] = 0
+            check_decode(c, m, host(q), topk, got=(o, l))
+            c.lengths[1] = m.lengths[1] = 700
         c.table[2] = -1  # no page at all
         o, l = cache_decode(c, q.cuda(), topk)
         assert not o[2].any() and torch.isneginf(l[:, 2]).all()
