@@ -120,7 +120,7 @@ int device_sm_count() {
 size_t page_ws_bytes(const moba_cache& c) { return 4 * cache::page_ws_words(c.num_pages, c.num_seqs); }
 
 struct DecodeLayout {
-    int hgroups, rows, max_items;
+    int hgroups, rows, row_heads, max_items;
     size_t items, tiles, done, part_o, part_ml, total;
 };
 
@@ -139,14 +139,15 @@ moba_status decode_layout(const moba_cache* c, int hq, int topk, DecodeLayout* L
     if (rows > (1LL << 24))
         return fail(MOBA_ERR_UNSUPPORTED, "num_seqs * num_q_heads too large (%lld rows of heads)", rows);
     L->rows = (int)rows;
-    const int most = (group < cache::kRowHeads ? group : cache::kRowHeads) * (topk - 1) + 1;
+    L->row_heads = group < cache::kRowHeads ? group : cache::kRowHeads;
+    const int most = L->row_heads * (topk - 1) + 1;
     L->max_items = topk == 0 ? 0 : most < c->max_blocks ? most : c->max_blocks;
     L->items = 0;
     L->tiles = align_up(sizeof(int2) * (size_t)L->rows * L->max_items);
     L->done = L->tiles + align_up(4ull * L->rows);
     L->part_o = L->done + align_up(4ull * L->rows);
-    L->part_ml = L->part_o + align_up(4ull * 2 * cache::kMaxCtas * cache::kRowHeads * c->head_dim);
-    L->total = L->part_ml + align_up(sizeof(float2) * 2 * cache::kMaxCtas * cache::kRowHeads);
+    L->part_ml = L->part_o + align_up(4ull * cache::kMaxParts * L->row_heads * c->head_dim);
+    L->total = L->part_ml + align_up(sizeof(float2) * cache::kMaxParts * L->row_heads);
     return MOBA_OK;
 }
 
@@ -224,6 +225,7 @@ moba_status moba_cache_decode(const moba_cache* c, const void* q, int num_q_head
     a.topk = topk;
     a.hgroups = L.hgroups;
     a.rows = L.rows;
+    a.row_heads = L.row_heads;
     a.max_items = L.max_items;
     a.scale_log2 = ldexpf(scale * 1.4426950408889634f, c->k_exp);
     a.out = static_cast<__nv_bfloat16*>(out);

@@ -20,7 +20,11 @@ namespace cache {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 64;
+#ifndef CFG_TILE
+#define CFG_TILE 64
+#endif
+constexpr int kTile = CFG_TILE;
+static_assert(kTile >= 16 && 64 % kTile == 0, "a page (a multiple of 128 tokens) holds at least two whole tiles");
 constexpr int kWindow = 1024;  // blocks scored at a time
 
 struct Row {
@@ -192,24 +196,37 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs
 // p <= 1 is rounded to fp16 (2^-11 relative, an eighth of the bf16 output's own rounding; below
 // 2^-14 an absolute 2^-25, against a sum of at least 1); the sum l is taken before that rounding.
 
-constexpr int kWarps = 8;
-constexpr int kStages = 2;
+constexpr int kWarps = kAttnWarps;
+constexpr int kSmem = 232448;  // shared memory of a CTA
 
+#ifndef CFG_DEPTH
+#define CFG_DEPTH 3
+#endif
+#ifndef CFG_SHORT
+#define CFG_SHORT 16
+#endif
+constexpr int kShortRow = CFG_SHORT;  // rows of fewer tiles than this on average go to single warps
+constexpr float kLag = 8.f;
+
+// A tile in shared memory.
 template <int D>
 struct Tile {
     static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / kGroup;
-    static constexpr int kK = 0, kKs = kCodes, kV = kKs + kScales, kVs = kV + kCodes;
-    static constexpr int kBytes = 2 * (kCodes + kScales);
+    static constexpr int kK = 0, kV = kCodes, kKs = 2 * kCodes, kVs = kKs + kScales, kBytes = kVs + kScales;
 };
+// Shared memory: flags and the scan, the warps' state of a segment, and each warp's ring of tiles
+// with their barriers and what they hold (tokens, heads).  The state holds a row's heads only, so
+// that layers with few query heads per KV head may get longer rings.
 template <int D>
 struct Smem {
-    static constexpr int kRing = 0;
-    static constexpr int kState = kRing + kWarps * kStages * Tile<D>::kBytes;  // [warps][heads][D] fp32
-    static constexpr int kMl = kState + kWarps * kRowHeads * D * 4;  // [warps][heads] float2
-    static constexpr int kMeta = kMl + kWarps * kRowHeads * 8;       // [warps][stages] int2
-    static constexpr int kBars = kMeta + kWarps * kStages * 8;
-    static constexpr int kMisc = kBars + kWarps * kStages * 8;  // scan and flags
-    static constexpr int kTotal = kMisc + 256;
+    static constexpr int kMisc = 0;  // abort flag, last flags, scan
+    static constexpr int kMl = 8 + 4 * kWarps + 24 * kWarps;   // [warps][heads] float2
+    static constexpr int kState = (kMl + kWarps * kRowHeads * 8 + 127) / 128 * 128;  // [warps][row heads][D] fp32
+    __host__ __device__ static int ring(int heads) { return kState + kWarps * heads * D * 4; }
+    __host__ __device__ static int depth(int heads) {  // tiles of a warp's ring
+        const int n = (kSmem - ring(heads)) / (kWarps * (Tile<D>::kBytes + 16));
+        return n < CFG_DEPTH ? n : CFG_DEPTH;
+    }
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -220,53 +237,45 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Plain loads (not inline assembly), so that the compiler may move them up to the last wait.
 template <int N>
-__device__ __forceinline__ void lds(uint32_t (&w)[N], uint32_t addr) {
-    if constexpr (N == 4)
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(addr));
-    else if constexpr (N == 2)
-        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-    else
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-    uint32_t x;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr));
-    return x;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-    uint32_t x;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(addr));
-    return x;
+__device__ __forceinline__ void lds(uint32_t (&w)[N], const unsigned char* at) {
+    if constexpr (N == 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(at);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (N == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(at);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(at);
+    }
 }
 
-// The tiles of a CTA: [begin, end) of all rows' tiles in order.  A segment is the part of a row
-// within it.
+// A team is a CTA's warps or, where rows are short, one warp.  Its tiles are [begin, end) of all
+// rows' tiles in order, warp i of the team taking every i-th; a segment is the part of a row in it.
 struct Segment {
     int row, at, t0, n;  // row; first tile as counted from begin; as counted in the row; tiles
+    int row_n;           // tiles of the whole row
 };
 __device__ __forceinline__ void next_segment(Segment& s, const int* __restrict__ tiles, int total) {
     s.at += s.n;
     s.t0 = 0;
-    do s.n = __ldcg(tiles + ++s.row);
-    while (s.n == 0);
-    s.n = min(s.n, total - s.at);
+    do s.row_n = __ldcg(tiles + ++s.row);
+    while (s.row_n == 0);
+    s.n = min(s.row_n, total - s.at);
 }
 
 template <int D>
@@ -280,10 +289,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
     const uint32_t base = ptx::smem_u32(smem);
     volatile int* abort_flag = reinterpret_cast<int*>(smem + S::kMisc);
-    long long* scan = reinterpret_cast<long long*>(smem + S::kMisc + 8);  // warp sums, then (first row, its start)
-    const uint32_t bars = base + S::kBars + warp * kStages * 8;
-    if (lane == 0) {
-        for (int i = 0; i < kStages; ++i) ptx::mbar_init(bars + 8 * i, 1);
+    long long* scan = reinterpret_cast<long long*>(smem + S::kMisc + 8 + 4 * kWarps);
+    const int depth = S::depth(a.row_heads);  // the warp's ring, its barriers and metas
+    const int ring = S::ring(a.row_heads) + warp * depth * T::kBytes;
+    const int bars = S::ring(a.row_heads) + kWarps * depth * T::kBytes + warp * depth * 16, metas = bars + 8 * depth;
+    if (lane < depth) {
+        ptx::mbar_init(base + bars + 8 * lane, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 0) *abort_flag = 0;
@@ -307,309 +318,377 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
         if (i < warp) before += scan[i];
         all_tiles += scan[i];
     }
-    // CTAs that work: at least one tile for each warp where there are that few
-    const long long ctas = max(1LL, min((long long)gridDim.x, (all_tiles + kWarps - 1) / kWarps));
-    const long long begin = blockIdx.x * all_tiles / ctas, end = (blockIdx.x + 1) * all_tiles / ctas;
-    if (blockIdx.x >= ctas || begin >= end) return;
+    // Rows of few tiles go to single warps, so that no warp waits for its CTA at every row's end.
+    const int tn = all_tiles < (long long)kShortRow * a.rows && a.rows > gridDim.x ? 1 : kWarps;
+    const int tw = tn == 1 ? 0 : warp, team = tn == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
+    const int members = tn * 32, me = tn == 1 ? lane : tid;
+    // teams that work: a tile at least for each warp where there are that few
+    const long long teams = max(1LL, min((long long)gridDim.x * (kWarps / tn), (all_tiles + tn - 1) / tn));
+    const long long share = all_tiles / teams, extra = all_tiles - share * teams;  // the first `extra` have one more
+    const long long begin = team * share + min((long long)team, extra), end = begin + share + (team < extra);
+    // the thread that holds a team's first tile's row finds it
     __syncthreads();
-    if (before <= begin && begin < before + mine) {
-        long long at = before;
-        int r = r0;
-        for (int n; at + (n = __ldcg(ws.tiles + r)) <= begin; ++r) at += n;
-        scan[kWarps] = r;
-        scan[kWarps + 1] = at;
+    if (me == 0) scan[tn == 1 ? warp : 0] = team < teams && begin < end ? begin : -1;
+    __syncthreads();
+    for (int i = 0; i < kWarps / tn; ++i) {
+        const long long b = scan[i];
+        if (before <= b && b < before + mine) {
+            long long at = before;
+            int r = r0;
+            for (int n; at + (n = __ldcg(ws.tiles + r)) <= b; ++r) at += n;
+            scan[kWarps + 2 * i] = r;
+            scan[kWarps + 2 * i + 1] = at;
+        }
     }
     __syncthreads();
+    if (team >= teams || begin >= end) return;
+    auto sync_team = [&]() {
+        if (tn == 1) __syncwarp();
+        else __syncthreads();
+    };
     const int total = (int)(end - begin);
     Segment seg;
-    seg.row = (int)scan[kWarps];
-    long long row_start = scan[kWarps + 1];  // first tile of seg's row among all tiles
+    seg.row = (int)scan[kWarps + (tn == 1 ? 2 * warp : 0)];
+    long long row_start = scan[kWarps + (tn == 1 ? 2 * warp + 1 : 1)];  // first tile of seg's row among all tiles
     seg.at = 0;
     seg.t0 = (int)(begin - row_start);
-    seg.n = min(__ldcg(ws.tiles + seg.row) - seg.t0, total);
+    seg.row_n = __ldcg(ws.tiles + seg.row);
+    seg.n = min(seg.row_n - seg.t0, total);
 
-    // The copies run ahead of the products on a cursor of their own.
+    // The warp's tiles go round its ring, fetched on a cursor of its own; a tile's page is looked up
+    // when the tile before it is fetched.
     const int per_block = c.chunk / kTile;
+    const uint32_t inv_block = 0xffffffffu / per_block + 1;  // tile * inv >> 32 is tile / per_block or 1 more
+    const size_t code_page = (size_t)c.hkv * c.chunk * (D / 2);
+    // lanes 0..3 copy the K codes, V codes, K scales and V scales (a scale per 8 bytes of codes)
+    const uint8_t* copy_src = lane == 0 ? c.kc : lane == 1 ? c.vc : lane == 2 ? c.ks : c.vs;
+    const uint32_t copy_dst = base + ring + (lane == 0 ? T::kK : lane == 1 ? T::kV : lane == 2 ? T::kKs : T::kVs);
+    const uint32_t copy_bytes = lane < 2 ? T::kCodes : T::kScales, copy_shift = lane < 2 ? 0 : 3;
     Segment ahead = seg;
-    Row arow = row_of(c, a, ahead.row);
-    int alen = held_tokens(c, arow.seq);
-    int issued = 0;
-    bool alive = true;
-    auto issue = [&]() {
-        const int i = warp + issued * kWarps;
-        if (i >= total || !alive) return;
-        if (i >= ahead.at + ahead.n) {
+    int next = tw;          // tile to fetch (INT_MAX after a wait that gave up), and where it goes
+    int next_slot = 0;
+    int pending = 0;        // tiles fetched and not taken
+    int2 item;              // its page and heads
+    int sub, valid;         // its place in its block, its tokens
+    int own_tile, own_len;  // first tile and tokens of the row's own block
+    int all_heads;
+    const int2* list;       // the row's list (topk = 0: of pages only)
+    size_t code_at;         // of the row's KV head in a page
+    auto look_up = [&]() {
+        if (next >= ahead.at + ahead.n) {
             do next_segment(ahead, ws.tiles, total);
-            while (i >= ahead.at + ahead.n);
-            arow = row_of(c, a, ahead.row);
-            alen = held_tokens(c, arow.seq);
+            while (next >= ahead.at + ahead.n);
+            own_tile = -1;
         }
-        const int tile = ahead.t0 + i - ahead.at, item = tile / per_block, sub = tile - item * per_block;
-        int2 it = make_int2(0, (1 << arow.nh) - 1);
-        if (a.topk)
-            it = __ldcg(ws.items + (size_t)ahead.row * a.max_items + item);
-        else
-            it.x = __ldg(c.table + (size_t)arow.seq * c.max_blocks + item);
-        const int last = (alen - 1) % c.chunk + 1 - sub * kTile;  // tokens left in an own block's tile
-        const bool own = ahead.t0 + i - ahead.at >= __ldcg(ws.tiles + ahead.row) - ((alen - 1) % c.chunk / kTile + 1);
-        int valid = own ? min(kTile, last) : kTile;
-        const int stage = issued % kStages;
-        const uint32_t dst = base + S::kRing + (warp * kStages + stage) * T::kBytes, bar = bars + 8 * stage;
-        if (it.x < 0 || it.x >= c.pages) valid = 0;
-        if (lane == 0) {
-            *reinterpret_cast<int2*>(smem + S::kMeta + (warp * kStages + stage) * 8) = make_int2(valid, it.y);
-            if (valid) {
-                const size_t cr = code_row(c, it.x, arow.g) + (size_t)sub * T::kCodes;
-                const size_t sr = scale_row(c, it.x, arow.g) + (size_t)sub * T::kScales;
-                ptx::mbar_arrive_tx(bar, T::kBytes);
-                bulk_load(dst + T::kK, c.kc + cr, T::kCodes, bar);
-                bulk_load(dst + T::kKs, c.ks + sr, T::kScales, bar);
-                bulk_load(dst + T::kV, c.vc + cr, T::kCodes, bar);
-                bulk_load(dst + T::kVs, c.vs + sr, T::kScales, bar);
-            } else {
-                ptx::mbar_arrive(bar);
-                report(c, MOBA_ERR_INVALID_ARG);
-            }
+        if (own_tile < 0) {
+            const Row w = row_of(c, a, ahead.row);
+            own_len = (held_tokens(c, w.seq) - 1) % c.chunk + 1;
+            own_tile = ahead.row_n - (own_len + kTile - 1) / kTile;
+            all_heads = (1 << w.nh) - 1;
+            list = a.topk ? ws.items + (size_t)ahead.row * a.max_items
+                          : reinterpret_cast<const int2*>(c.table + (size_t)w.seq * c.max_blocks);
+            code_at = (size_t)w.g * c.chunk * (D / 2);
         }
-        ++issued;
+        const int tile = ahead.t0 + next - ahead.at;
+        int block = __umulhi(tile, inv_block);
+        sub = tile - block * per_block;
+        if (sub < 0) --block, sub += per_block;
+        item = a.topk ? __ldcg(list + block) : make_int2(__ldg(reinterpret_cast<const int*>(list) + block), all_heads);
+        valid = tile >= own_tile ? min(kTile, own_len - sub * kTile) : kTile;
     };
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) issue();
+    auto fetch = [&]() {
+        if (next >= total) return;
+        const uint32_t bar = base + bars + 8 * next_slot;
+        const bool ok = (unsigned)item.x < (unsigned)c.pages;
+        if (lane == 0) {
+            *reinterpret_cast<int2*>(smem + metas + 8 * next_slot) =
+                make_int2(ok ? valid : 0, item.y | (valid < kTile || item.y != all_heads) << 8);
+            if (ok) ptx::mbar_arrive_tx(bar, T::kBytes);
+        }
+        __syncwarp();
+        if (ok) {
+            const size_t at = item.x * code_page + code_at + sub * T::kCodes;
+            if (lane < 4) bulk_load(copy_dst + next_slot * T::kBytes, copy_src + (at >> copy_shift), copy_bytes, bar);
+        } else if (lane == 0) {
+            ptx::mbar_arrive(bar);
+            report(c, MOBA_ERR_INVALID_ARG);
+        }
+        ++pending;
+        if (++next_slot == depth) next_slot = 0;
+        next += tn;
+        if (next < total) look_up();
+    };
+    own_tile = -1;
+    if (tw < total) look_up();
+    for (int i = 0; i < depth; ++i) fetch();
+    int slot = 0, phase = 0;  // of the tile to take
 
     float* state = reinterpret_cast<float*>(smem + S::kState);
     float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
-    int used = 0;  // tiles this warp has taken
+    int cur = tw;  // tile to take
     for (;;) {
         const Row w = row_of(c, a, seg.row);
-        // q's fragments: head g8, channels t4 * (D / 4) ..
-        uint32_t qf[D / 8];
-        float unit;
-        {
-            uint32_t raw[D / 8];
-            const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)w.seq * a.hq + w.h0 + g8) * D + t4 * (D / 4));
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint4 x = g8 < w.nh ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                raw[4 * i] = x.x;
-                raw[4 * i + 1] = x.y;
-                raw[4 * i + 2] = x.z;
-                raw[4 * i + 3] = x.w;
-            }
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, raw[i] & 0x7fff7fffu);
-            top = max(top & 0xffffu, top >> 16);
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^(14 - e) for a largest magnitude in [2^e, 2^(e+1)), within fp32's normal range
-            const int fb = min(268 - (int)(top >> 7), 253);
-            const float f = __uint_as_float((uint32_t)fb << 23);
-            unit = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)(254 - fb) << 23), 1e-37f);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                qf[i] = pack_f16(__uint_as_float(raw[i] << 16) * f, __uint_as_float(raw[i] & 0xffff0000u) * f);
-        }
-        // this thread's columns of S^T and O^T are heads 2 t4 and 2 t4 + 1
-        const float unit0 = __shfl_sync(0xffffffffu, unit, 8 * t4), unit1 = __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
+        const bool takes = cur < seg.at + seg.n;  // this warp has tiles of the segment
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         float o[kMt][4];
 #pragma unroll
         for (int i = 0; i < kMt; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        if (takes) {
+            // q's fragments: head g8, channels t4 * (D / 4) ..
+            uint32_t qf[D / 8];
+            float unit;
+            {
+                uint32_t raw[D / 8];
+                const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)w.seq * a.hq + w.h0 + g8) * D + t4 * (D / 4));
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 x = g8 < w.nh ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                    raw[4 * i] = x.x;
+                    raw[4 * i + 1] = x.y;
+                    raw[4 * i + 2] = x.z;
+                    raw[4 * i + 3] = x.w;
+                }
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, raw[i] & 0x7fff7fffu);
+                top = max(top & 0xffffu, top >> 16);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^(14 - e) for a largest magnitude in [2^e, 2^(e+1)), within fp32's normal range
+                const int fb = min(268 - (int)(top >> 7), 253);
+                const float f = __uint_as_float((uint32_t)fb << 23);
+                unit = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)(254 - fb) << 23), 1e-37f);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    qf[i] = pack_f16(__uint_as_float(raw[i] << 16) * f, __uint_as_float(raw[i] & 0xffff0000u) * f);
+            }
+            // this thread's columns of S^T and O^T are heads 2 t4 and 2 t4 + 1
+            const float unit0 = __shfl_sync(0xffffffffu, unit, 8 * t4), unit1 = __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
 
-        for (; warp + used * kWarps < seg.at + seg.n; ++used) {
-            const int stage = used % kStages;
-            const uint32_t src = base + S::kRing + (warp * kStages + stage) * T::kBytes;
-            if (alive) alive = ptx::wait_bar(bars + 8 * stage, used / kStages & 1, abort_flag, c.status);
-            const int2 meta = *reinterpret_cast<const int2*>(smem + S::kMeta + (warp * kStages + stage) * 8);
-            if (alive && meta.x) {
-                const int valid = meta.x;
-                const bool on0 = meta.y >> (2 * t4) & 1, on1 = meta.y >> (2 * t4 + 1) & 1;
+            for (; cur < seg.at + seg.n; cur += tn) {
+                const uint32_t bar = base + bars + 8 * slot;
+                const int2 meta = *reinterpret_cast<const int2*>(smem + metas + 8 * slot);
+                unsigned char* src = smem + ring + slot * T::kBytes;
+                const int ntok = meta.x;
+                bool ok = true;
+                if (!__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, phase)))
+                    ok = next != INT_MAX && ptx::wait_bar(bar, phase, abort_flag, c.status);
+                if (!ok) {  // gave up, now or before: nothing more is fetched or taken
+                    next = INT_MAX;
+                    continue;
+                }
+                if (ntok) {
                 // Rows of the 8-row groups are taken in the order 0 1 2 3 5 4 7 6: the rows that
                 // one load reads, by g8 for K and by t4 for V, then fall into different banks.
                 const int kr = g8 ^ (g8 >> 2), va = (2 * t4) ^ (t4 >> 1), vb = (2 * t4 + 1) ^ (t4 >> 1);
-                float s[kTile / 16][4];
+                    float s[kTile / 16][4];
 #pragma unroll
-                for (int mt = 0; mt < kTile / 16; ++mt) {
-                    s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
-                    uint32_t x[2][kKw], sc[2][2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int key = mt * 16 + 8 * h + kr;
-                        lds<kKw>(x[h], src + T::kK + key * (D / 2) + t4 * (D / 8));
-                        if constexpr (D == 128) {
-                            const uint32_t two = e4m3x2_to_f16x2(lds_u16(src + T::kKs + key * 8 + 2 * t4));
-                            sc[h][0] = __byte_perm(two, 0, 0x1010);
-                            sc[h][1] = __byte_perm(two, 0, 0x3232);
-                        } else {
-                            const uint32_t one = lds_u8(src + T::kKs + key * 4 + t4);
-                            sc[h][0] = sc[h][1] = e4m3x2_to_f16x2(one | one << 8);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < kKw; ++i) {
-                        uint32_t lo[4], hi[4];
-                        e2m1x8_to_f16x2(x[0][i], lo);
-                        e2m1x8_to_f16x2(x[1][i], hi);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            lo[j] = hmul2(lo[j], sc[0][i / 2]);
-                            hi[j] = hmul2(hi[j], sc[1][i / 2]);
-                        }
-                        mma16816(s[mt], lo[0], hi[0], lo[1], hi[1], qf[4 * i], qf[4 * i + 1]);
-                        mma16816(s[mt], lo[2], hi[2], lo[3], hi[3], qf[4 * i + 2], qf[4 * i + 3]);
-                    }
-                }
-                float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-                for (int mt = 0; mt < kTile / 16; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const bool ok = mt * 16 + 8 * h + kr < valid;
-                        s[mt][2 * h] = ok && on0 ? s[mt][2 * h] : -INFINITY;
-                        s[mt][2 * h + 1] = ok && on1 ? s[mt][2 * h + 1] : -INFINITY;
-                        x0 = fmaxf(x0, s[mt][2 * h]);
-                        x1 = fmaxf(x1, s[mt][2 * h + 1]);
-                    }
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) {
-                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
-                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
-                }
-                const float n0 = fmaxf(m0, x0 * unit0), n1 = fmaxf(m1, x1 * unit1);
-                const float ref0 = n0 == -INFINITY ? 0.f : n0, ref1 = n1 == -INFINITY ? 0.f : n1;
-                const float al0 = ptx::ex2(m0 - ref0), al1 = ptx::ex2(m1 - ref1);
-                m0 = n0;
-                m1 = n1;
-                if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
-                    l0 *= al0;
-                    l1 *= al1;
-#pragma unroll
-                    for (int i = 0; i < kMt; ++i) {
-                        o[i][0] *= al0;
-                        o[i][1] *= al1;
-                        o[i][2] *= al0;
-                        o[i][3] *= al1;
-                    }
-                }
-                uint32_t p[kTile / 16][2];
-#pragma unroll
-                for (int mt = 0; mt < kTile / 16; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float p0 = ptx::ex2(fmaf(s[mt][2 * h], unit0, -ref0));
-                        const float p1 = ptx::ex2(fmaf(s[mt][2 * h + 1], unit1, -ref1));
-                        l0 += p0;
-                        l1 += p1;
-                        p[mt][h] = transpose8x8(pack_f16(p0, p1));
-                    }
-#pragma unroll
-                for (int mt = 0; mt < kTile / 16; ++mt) {
-                    // keys va, vb of the step's rows 0..7 and of its rows 8..15
-                    uint32_t x[4][kVw], sc[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int ka = mt * 16 + 8 * h + va, kb = mt * 16 + 8 * h + vb;
-                        lds<kVw>(x[2 * h], src + T::kV + ka * (D / 2) + g8 * (D / 16));
-                        lds<kVw>(x[2 * h + 1], src + T::kV + kb * (D / 2) + g8 * (D / 16));
-                        const int group = D == 128 ? g8 : g8 >> 1;
-                        uint32_t sa = lds_u8(src + T::kVs + ka * (D / kGroup) + group);
-                        uint32_t sb = lds_u8(src + T::kVs + kb * (D / kGroup) + group);
-                        sa = ka < valid ? sa : 0;  // what lies behind the last token may be anything
-                        sb = kb < valid ? sb : 0;
-                        sc[h] = e4m3x2_to_f16x2(sa | sb << 8);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kVw; ++i) {
-                        uint32_t e[2][4], f[2][4];  // even and odd channels, by rows' half
+                    for (int mt = 0; mt < kTile / 16; ++mt) {
+                        s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
+                        uint32_t x[2][kKw], sc[2][2];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t ra = x[2 * h][i], rb = x[2 * h + 1][i];
-                            e2m1x8_to_f16x2((ra & 0x0f0f0f0fu) | (rb << 4 & 0xf0f0f0f0u), e[h]);
-                            e2m1x8_to_f16x2((ra >> 4 & 0x0f0f0f0fu) | (rb & 0xf0f0f0f0u), f[h]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                e[h][j] = hmul2(e[h][j], sc[h]);
-                                f[h][j] = hmul2(f[h][j], sc[h]);
+                            const int key = mt * 16 + 8 * h + kr;
+                            lds<kKw>(x[h], src + key * (D / 2) + t4 * (D / 8));
+                            if constexpr (D == 128) {
+                                const uint32_t two = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(src + T::kKs + key * 8 + 2 * t4));
+                                sc[h][0] = __byte_perm(two, 0, 0x1010);
+                                sc[h][1] = __byte_perm(two, 0, 0x3232);
+                            } else {
+                                const uint32_t one = src[T::kKs + key * 4 + t4];
+                                sc[h][0] = sc[h][1] = e4m3x2_to_f16x2(one | one << 8);
                             }
                         }
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma16816(o[4 * i + j], e[0][j], f[0][j], e[1][j], f[1][j], p[mt][0], p[mt][1]);
+                        for (int i = 0; i < kKw; ++i) {
+                            uint32_t lo[4], hi[4];
+                            e2m1x8_to_f16x2(x[0][i], lo);
+                            e2m1x8_to_f16x2(x[1][i], hi);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                lo[j] = hmul2(lo[j], sc[0][i / 2]);
+                                hi[j] = hmul2(hi[j], sc[1][i / 2]);
+                            }
+                            mma16816(s[mt], lo[0], hi[0], lo[1], hi[1], qf[4 * i], qf[4 * i + 1]);
+                            mma16816(s[mt], lo[2], hi[2], lo[3], hi[3], qf[4 * i + 2], qf[4 * i + 3]);
+                        }
+                    }
+                    if (meta.y >> 8) {  // tokens behind the last one, heads that did not choose the block
+                        const bool on0 = meta.y >> (2 * t4) & 1, on1 = meta.y >> (2 * t4 + 1) & 1;
+#pragma unroll
+                        for (int mt = 0; mt < kTile / 16; ++mt)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const bool ok = mt * 16 + 8 * h + kr < ntok;
+                                s[mt][2 * h] = ok && on0 ? s[mt][2 * h] : -INFINITY;
+                                s[mt][2 * h + 1] = ok && on1 ? s[mt][2 * h + 1] : -INFINITY;
+                            }
+                    }
+                    float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
+#pragma unroll
+                    for (int mt = 1; mt < kTile / 16; ++mt) {
+                        x0 = ptx::fmax3(x0, s[mt][0], s[mt][2]);
+                        x1 = ptx::fmax3(x1, s[mt][1], s[mt][3]);
+                    }
+                    // The reference of the exponentials follows the maximum only when a score passes it by
+                    // 2^kLag: p <= 2^kLag stays in fp16's range, and most tiles need no reduction over the
+                    // warp and no rescaling.
+                    if (__any_sync(0xffffffffu, x0 * unit0 > m0 + kLag || x1 * unit1 > m1 + kLag)) {
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) {
+                            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+                            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+                        }
+                        const float n0 = fmaxf(m0, x0 * unit0), n1 = fmaxf(m1, x1 * unit1);
+                        const float al0 = ptx::ex2(m0 - (n0 == -INFINITY ? 0.f : n0));
+                        const float al1 = ptx::ex2(m1 - (n1 == -INFINITY ? 0.f : n1));
+                        m0 = n0;
+                        m1 = n1;
+                        l0 *= al0;
+                        l1 *= al1;
+#pragma unroll
+                        for (int i = 0; i < kMt; ++i) {
+                            o[i][0] *= al0;
+                            o[i][1] *= al1;
+                            o[i][2] *= al0;
+                            o[i][3] *= al1;
+                        }
+                    }
+                    const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
+                    uint32_t p[kTile / 16][2];
+#pragma unroll
+                    for (int mt = 0; mt < kTile / 16; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float p0 = ptx::ex2(fmaf(s[mt][2 * h], unit0, -ref0));
+                            const float p1 = ptx::ex2(fmaf(s[mt][2 * h + 1], unit1, -ref1));
+                            l0 += p0;
+                            l1 += p1;
+                            p[mt][h] = transpose8x8(pack_f16(p0, p1));
+                        }
+                    if (ntok < kTile) {  // what lies behind the last token may be anything: scale 0
+                        uint16_t* tail = reinterpret_cast<uint16_t*>(src + T::kVs);
+                        for (int i = ntok * (D / kGroup / 2) + lane; i < kTile * (D / kGroup / 2); i += 32) tail[i] = 0;
+                        ptx::fence_proxy_async();  // before a later copy into these bytes
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < kTile / 16; ++mt) {
+                        // keys va, vb of the step's rows 0..7 and of its rows 8..15
+                        uint32_t x[4][kVw], sc[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int ka = mt * 16 + 8 * h + va, kb = mt * 16 + 8 * h + vb;
+                            lds<kVw>(x[2 * h], src + T::kV + ka * (D / 2) + g8 * (D / 16));
+                            lds<kVw>(x[2 * h + 1], src + T::kV + kb * (D / 2) + g8 * (D / 16));
+                            const int group = D == 128 ? g8 : g8 >> 1;
+                            const uint32_t sa = src[T::kVs + ka * (D / kGroup) + group];
+                            const uint32_t sb = src[T::kVs + kb * (D / kGroup) + group];
+                            sc[h] = e4m3x2_to_f16x2(sa | sb << 8);
+                        }
+#pragma unroll
+                        for (int i = 0; i < kVw; ++i) {
+                            uint32_t e[2][4], f[2][4];  // even and odd channels, by rows' half
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t ra = x[2 * h][i], rb = x[2 * h + 1][i];
+                                e2m1x8_to_f16x2((ra & 0x0f0f0f0fu) | (rb << 4 & 0xf0f0f0f0u), e[h]);
+                                e2m1x8_to_f16x2((ra >> 4 & 0x0f0f0f0fu) | (rb & 0xf0f0f0f0u), f[h]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    e[h][j] = hmul2(e[h][j], sc[h]);
+                                    f[h][j] = hmul2(f[h][j], sc[h]);
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                mma16816(o[4 * i + j], e[0][j], f[0][j], e[1][j], f[1][j], p[mt][0], p[mt][1]);
+                        }
                     }
                 }
+                __syncwarp();
+                --pending;
+                fetch();
+                if (++slot == depth) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
-            __syncwarp();
-            issue();
-        }
 
-        // The warps' parts of the segment, then the CTA's.
+            // this warp's part of the segment
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, off);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, off);
-        }
-        if (g8 == 0) {
-            ml[warp * kRowHeads + 2 * t4] = make_float2(m0, l0);
-            ml[warp * kRowHeads + 2 * t4 + 1] = make_float2(m1, l1);
-        }
-        float* mine_o = state + (warp * kRowHeads + 2 * t4) * D + g8 * (D / 8);
+            for (int off = 4; off < 32; off <<= 1) {
+                l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+                l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+            }
+            if (g8 == 0) {
+                ml[warp * kRowHeads + 2 * t4] = make_float2(m0, l0);
+                ml[warp * kRowHeads + 2 * t4 + 1] = make_float2(m1, l1);
+            }
+            float* mine_o = state + (warp * a.row_heads + 2 * t4) * D + g8 * (D / 8);
 #pragma unroll
-        for (int i = 0; i < kMt; ++i) {
-            *reinterpret_cast<float2*>(mine_o + 2 * i) = make_float2(o[i][0], o[i][2]);
-            *reinterpret_cast<float2*>(mine_o + D + 2 * i) = make_float2(o[i][1], o[i][3]);
+            for (int i = 0; i < kMt; ++i) {
+                if (2 * t4 < w.nh) *reinterpret_cast<float2*>(mine_o + 2 * i) = make_float2(o[i][0], o[i][2]);
+                if (2 * t4 + 1 < w.nh) *reinterpret_cast<float2*>(mine_o + D + 2 * i) = make_float2(o[i][1], o[i][3]);
+            }
         }
-        __syncthreads();
-        const bool whole = seg.t0 == 0 && seg.n == __ldcg(ws.tiles + seg.row);
-        const int slot = 2 * blockIdx.x + (seg.at > 0);
-        for (int i = tid; i < w.nh * D; i += kWarps * 32) {
+        sync_team();
+        // The team's: the warps that took tiles are those of the segment's first tn tiles.
+        const int parts = min(seg.n, tn), first = tn == 1 ? warp : seg.at % tn;
+        const bool whole = seg.n == seg.row_n;
+        const int part = 2 * team + (seg.at > 0);
+        for (int i = me; i < w.nh * D; i += members) {
             const int h = i / D, e = i - h * D;
             float m = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) m = fmaxf(m, ml[k * kRowHeads + h].x);
+            for (int k = 0, j = first; k < parts; ++k, j = j + 1 == tn ? 0 : j + 1) m = fmaxf(m, ml[j * kRowHeads + h].x);
             const float ref = m == -INFINITY ? 0.f : m;
             float l = 0.f, acc = 0.f;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const float2 x = ml[k * kRowHeads + h];
+            for (int k = 0, j = first; k < parts; ++k, j = j + 1 == tn ? 0 : j + 1) {
+                const float2 x = ml[j * kRowHeads + h];
                 const float f = ptx::ex2(x.x - ref);
                 l = fmaf(f, x.y, l);
-                acc = fmaf(f, state[(k * kRowHeads + h) * D + e], acc);
+                acc = fmaf(f, state[(j * a.row_heads + h) * D + e], acc);
             }
             if (whole) {
                 a.out[((size_t)w.seq * a.hq + w.h0 + h) * D + e] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l * c.v_unit);
                 if (e == 0) a.lse[(size_t)(w.h0 + h) * c.seqs + w.seq] = m * 0.69314718055994531f + logf(l);
             } else {
-                ws.part_o[((size_t)slot * kRowHeads + h) * D + e] = acc;
-                if (e == 0) ws.part_ml[slot * kRowHeads + h] = make_float2(m, l);
+                ws.part_o[((size_t)part * a.row_heads + h) * D + e] = acc;
+                if (e == 0) ws.part_ml[part * a.row_heads + h] = make_float2(m, l);
             }
         }
         if (!whole) {
-            // parts come from the CTAs that hold the row's first to last tile
-            const int n_row = __ldcg(ws.tiles + seg.row);
-            const int c0 = (int)(((row_start + 1) * ctas - 1) / all_tiles);
-            const int c1 = (int)(((row_start + n_row) * ctas - 1) / all_tiles);
-            int* last = reinterpret_cast<int*>(smem + S::kMisc + 4);
+            // Parts come from the teams that hold the row's first to last tile; the last team to write
+            // its part adds all of them in order.
+            auto holder = [&](long long tile) {
+                const long long longer = extra * (share + 1);
+                return (int)(tile < longer ? tile / (share + 1) : extra + (tile - longer) / share);
+            };
+            const int c0 = holder(row_start), c1 = holder(row_start + seg.row_n - 1);
+            int* last = reinterpret_cast<int*>(smem + S::kMisc + 8) + (tn == 1 ? warp : 0);
             __threadfence();
-            __syncthreads();
-            if (tid == 0) *last = atomicAdd(ws.done + seg.row, 1) == c1 - c0;
-            __syncthreads();
+            sync_team();
+            if (me == 0) *last = atomicAdd(ws.done + seg.row, 1) == c1 - c0;
+            sync_team();
             if (*last) {
                 __threadfence();
-                for (int i = tid; i < w.nh * D; i += kWarps * 32) {
+                // only the first part can begin behind its team's first tile (the second slot)
+                const int skew = row_start > c0 * share + min((long long)c0, extra);
+                for (int i = me; i < w.nh * D; i += members) {
                     const int h = i / D, e = i - h * D;
                     float m = -INFINITY;
-                    for (int k = c0; k <= c1; ++k) {
-                        const int sl = 2 * k + (row_start > k * all_tiles / ctas);
-                        m = fmaxf(m, __ldcg(ws.part_ml + sl * kRowHeads + h).x);
-                    }
+#pragma unroll 8
+                    for (int k = c0; k <= c1; ++k)
+                        m = fmaxf(m, __ldcg(ws.part_ml + (2 * k + (k == c0 ? skew : 0)) * a.row_heads + h).x);
                     const float ref = m == -INFINITY ? 0.f : m;
                     float l = 0.f, acc = 0.f;
+#pragma unroll 8
                     for (int k = c0; k <= c1; ++k) {
-                        const int sl = 2 * k + (row_start > k * all_tiles / ctas);
-                        const float2 x = __ldcg(ws.part_ml + sl * kRowHeads + h);
+                        const size_t sl = (size_t)(2 * k + (k == c0 ? skew : 0)) * a.row_heads + h;
+                        const float2 x = __ldcg(ws.part_ml + sl);
                         const float f = ptx::ex2(x.x - ref);
                         l = fmaf(f, x.y, l);
-                        acc = fmaf(f, __ldcg(ws.part_o + ((size_t)sl * kRowHeads + h) * D + e), acc);
+                        acc = fmaf(f, __ldcg(ws.part_o + sl * D + e), acc);
                     }
                     a.out[((size_t)w.seq * a.hq + w.h0 + h) * D + e] =
                         __float2bfloat16_rn(l == 0.f ? 0.f : acc / l * c.v_unit);
@@ -620,12 +699,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
         if (seg.at + seg.n >= total) break;
         row_start += seg.t0 + seg.n;  // a segment that another follows ends its row
         next_segment(seg, ws.tiles, total);
-        __syncthreads();  // the state is free again
+        sync_team();  // the state is free again
     }
-    // after a wait that gave up: the copies still in flight land before the memory is given back
-    if (!alive)
-        for (int k = used > kStages ? issued - kStages : 0; k < issued; ++k)
-            ptx::drain_bar(bars + 8 * (k % kStages), k / kStages & 1);
+    // After a wait that gave up, the copies still in flight land before the memory is given back.
+    if (next == INT_MAX)
+        for (int i = 0; i < pending; ++i) {
+            ptx::drain_bar(base + bars + 8 * slot, phase);
+            if (++slot == depth) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
 }
 
 template <int D>
@@ -641,9 +725,9 @@ cudaError_t launch_decode_d(const View& c, const DecodeArgs& a, const DecodeWs& 
         cache_plan_kernel<D, 32><<<a.rows, kThreads, 0, st>>>(c, a, ws);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+    e = cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    cache_attn_kernel<D><<<min(num_sms, kMaxCtas), kWarps * 32, Smem<D>::kTotal, st>>>(c, a, ws);
+    cache_attn_kernel<D><<<min(num_sms, kMaxCtas), kWarps * 32, kSmem, st>>>(c, a, ws);
     return cudaGetLastError();
 }
 

@@ -108,19 +108,24 @@ struct DecodeArgs {
     int hq, group, topk;
     int hgroups;     // rows per (sequence, KV head): ceil(group / kRowHeads)
     int rows;        // seqs * hkv * hgroups
+    int row_heads;   // min(group, kRowHeads)
     int max_items;   // most blocks of one row's list
     float scale_log2;  // softmax scale * log2 e * 2^k_exp
     __nv_bfloat16* out;
     float* lse;
 };
-// CTAs of the attention kernel at most (it runs as many as the device holds at once).
-constexpr int kMaxCtas = 296;
+// CTAs of the attention kernel at most (one per SM), its warps, and the parts of rows that they
+// may leave to be merged: two per team of warps (csrc/cache_decode.cu).
+#ifndef CFG_WARPS
+#define CFG_WARPS 12
+#endif
+constexpr int kMaxCtas = 160, kAttnWarps = CFG_WARPS, kMaxParts = 2 * kMaxCtas * kAttnWarps;
 struct DecodeWs {
     int2* items;     // [rows, max_items]: (page, heads that attend to it), ascending blocks
     int* tiles;      // [rows]: tiles of each row
-    int* done;       // [rows]: CTAs that have written their part of the row
-    float* part_o;   // [2 * kMaxCtas, kRowHeads, d]: unnormalised outputs of a row's part
-    float2* part_ml;  // [2 * kMaxCtas, kRowHeads]: its running maximum (log2 units) and sum
+    int* done;       // [rows]: teams that have written their part of the row
+    float* part_o;   // [kMaxParts, row heads, d]: unnormalised outputs of a row's part
+    float2* part_ml;  // [kMaxParts, row heads]: its running maximum (log2 units) and sum
 };
 cudaError_t launch_decode(const View& c, const DecodeArgs& a, const DecodeWs& ws, int num_sms, cudaStream_t st);
 
