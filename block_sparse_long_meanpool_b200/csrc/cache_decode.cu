@@ -10,6 +10,8 @@
 //                      64-token tiles; a row that several CTAs share is merged by the last of them
 #include <climits>
 
+#include <cooperative_groups.h>
+
 #include "cache_internal.cuh"
 #include "moba_internal.cuh"
 #include "ptx.cuh"
@@ -47,84 +49,11 @@ __device__ __forceinline__ int held_tokens(const View& c, int seq) {
     return L < 0 || L > (long long)c.max_blocks * c.chunk ? 0 : L;
 }
 
-// items[row] lists the row's blocks ascending, the own block last, as (page, heads that attend)
-// (not written for topk = 0: the row's blocks are the table's); tiles[row] is the number of its
-// tiles, 0 for an empty sequence, whose outputs are written here.
-template <int D, int K>
-__global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs a, DecodeWs ws) {
-    constexpr int V = D / 32;
-    __shared__ float qs[kRowHeads][D];
-    __shared__ float score[kRowHeads][kWindow];
-    __shared__ int pick[kRowHeads * 32];
-    const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Row w = row_of(c, a, r);
-    const int L = held_tokens(c, w.seq);
-    if (L == 0) {
-        if (tid == 0) {
-            ws.tiles[r] = 0;
-            if (__ldg(c.lengths + w.seq) != 0) report(c, MOBA_ERR_INVALID_ARG);
-        }
-        for (int i = tid; i < w.nh * D; i += kThreads)
-            a.out[((size_t)w.seq * a.hq + w.h0) * D + i] = __float2bfloat16(0.f);
-        if (tid < w.nh) a.lse[(size_t)(w.h0 + tid) * c.seqs + w.seq] = -INFINITY;
-        return;
-    }
-    const int own = (L - 1) / c.chunk;
-    const int* row = c.table + (size_t)w.seq * c.max_blocks;
-    int2* items = ws.items + (size_t)r * a.max_items;
-    const int all = (1 << w.nh) - 1;
-    const int own_tiles = (L - own * c.chunk + kTile - 1) / kTile, per_block = c.chunk / kTile;
-    if (tid == 0) ws.done[r] = 0;
-    const int n_route = min(a.topk - 1, own);
-    if (a.topk == 0 || n_route == own) {  // every block
-        if (tid == 0) ws.tiles[r] = own * per_block + own_tiles;
-        if (a.topk)
-            for (int j = tid; j <= own; j += kThreads) items[j] = make_int2(__ldg(row + j), all);
-        return;
-    }
-    for (int i = tid; i < kRowHeads * D; i += kThreads) {
-        const int h = i / D;
-        qs[h][i - h * D] = h < w.nh ? __bfloat162float(a.q[((size_t)w.seq * a.hq + w.h0) * D + i]) : 0.f;
-    }
-    float val[K];
-    int idx[K];
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-        val[i] = -INFINITY;
-        idx[i] = INT_MAX;
-    }
-    for (int j0 = 0; j0 < own; j0 += kWindow) {
-        const int n = min(kWindow, own - j0);
-        __syncthreads();
-        for (int j = warp; j < n; j += kThreads / 32) {
-            const int page = __ldg(row + j0 + j);
-            const bool ok = page >= 0 && page < c.pages;
-            float s[kRowHeads];
-#pragma unroll
-            for (int h = 0; h < kRowHeads; ++h) s[h] = 0.f;
-            if (ok) {
-                const float* m = c.mean + ((size_t)page * c.hkv + w.g) * D + lane * V;
-                float x[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[i] = __ldg(m + i);
-#pragma unroll
-                for (int h = 0; h < kRowHeads; ++h)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) s[h] = fmaf(qs[h][lane * V + i], x[i], s[h]);
-            }
-#pragma unroll
-            for (int h = 0; h < kRowHeads; ++h) {
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], off);
-                // a NaN, and a page that is not there, ranks last
-                if (lane == 0) score[h][j] = ok && s[h] == s[h] ? s[h] : -INFINITY;
-            }
-        }
-        __syncthreads();
-        for (int j = lane; j < n; j += 32) insert_ordered<K>(val, idx, score[warp][j], j0 + j);
-    }
-    // warp = head: n_route rounds of a warp argmax over the lists' heads, (score desc, block asc)
-    for (int i = 0; i < n_route; ++i) {
+// Inserts a warp's candidates (lane by lane) into its sorted lists' best n, by n rounds of a warp
+// argmax over the lists' heads in the order (score descending, block ascending): out(i, score, block).
+template <int K, typename F>
+__device__ __forceinline__ void take_best(float (&val)[K], int (&idx)[K], int n, F out) {
+    for (int i = 0; i < n; ++i) {
         float bv = val[0];
         int bi = idx[0];
 #pragma unroll
@@ -145,7 +74,146 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs
             val[K - 1] = -INFINITY;
             idx[K - 1] = INT_MAX;
         }
-        if (lane == 0) pick[warp * n_route + i] = bi;
+        out(i, bv, bi);
+    }
+}
+
+// items[row] lists the row's blocks ascending, the own block last, as (page, heads that attend)
+// (not written for topk = 0: the row's blocks are the table's); tiles[row] is the number of its
+// tiles, 0 for an empty sequence, whose outputs are written here.
+// The CTAs of a cluster share a row: each scores a part of its blocks and lists its heads' best,
+// and the first one picks from the lists.  Eight lanes take a block (a row of k_mean: D fp32, read
+// in 128-byte pieces), a warp kBatch blocks for each of its four groups of lanes at a time, so that
+// a CTA has 64 rows in flight; what bounds the kernel is their latency, not their bytes.
+constexpr int kBatch = 2;
+template <int D, int K>
+__global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs a, DecodeWs ws) {
+    constexpr int V = D / 32;  // float4s of a lane
+    __shared__ float4 qs[kRowHeads][D / 4];
+    __shared__ float score[kRowHeads][kWindow];
+    __shared__ float best_v[kRowHeads * 32];
+    __shared__ int best_i[kRowHeads * 32];
+    __shared__ int pick[kRowHeads * 32];
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int cs = cluster.num_blocks(), rank = cluster.block_rank();
+    cudaTriggerProgrammaticLaunchCompletion();
+    const int r = blockIdx.x / cs, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Row w = row_of(c, a, r);
+    const int L = held_tokens(c, w.seq);
+    if (L == 0) {
+        if (rank) return;
+        if (tid == 0) {
+            ws.tiles[r] = 0;
+            if (__ldg(c.lengths + w.seq) != 0) report(c, MOBA_ERR_INVALID_ARG);
+        }
+        for (int i = tid; i < w.nh * D; i += kThreads)
+            a.out[((size_t)w.seq * a.hq + w.h0) * D + i] = __float2bfloat16(0.f);
+        if (tid < w.nh) a.lse[(size_t)(w.h0 + tid) * c.seqs + w.seq] = -INFINITY;
+        return;
+    }
+    const int own = (L - 1) / c.chunk;
+    const int* row = c.table + (size_t)w.seq * c.max_blocks;
+    int2* items = ws.items + (size_t)r * a.max_items;
+    const int all = (1 << w.nh) - 1;
+    const int own_tiles = (L - own * c.chunk + kTile - 1) / kTile, per_block = c.chunk / kTile;
+    if (tid == 0 && rank == 0) ws.done[r] = 0;
+    const int n_route = min(a.topk - 1, own);
+    if (a.topk <= 1 || n_route == own) {  // every block, or the own one only
+        if (rank) return;
+        const int first = a.topk == 1 ? own : 0;
+        if (tid == 0) ws.tiles[r] = (own - first) * per_block + own_tiles;
+        if (a.topk)
+            for (int j = first + tid; j <= own; j += kThreads) items[j - first] = make_int2(__ldg(row + j), all);
+        return;
+    }
+    for (int i = tid; i < kRowHeads * D; i += kThreads) {
+        const int h = i / D;
+        reinterpret_cast<float*>(qs)[i] = h < w.nh ? __bfloat162float(a.q[((size_t)w.seq * a.hq + w.h0) * D + i]) : 0.f;
+    }
+    float val[K];
+    int idx[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        val[i] = -INFINITY;
+        idx[i] = INT_MAX;
+    }
+    const int l8 = lane & 7;
+    const int span = min(kWindow, (own + cs - 1) / cs);
+    for (int start = rank * span; start < own; start += cs * span) {
+        const int n = min(span, own - start);
+        __syncthreads();
+        for (int b = (warp * 4 + (lane >> 3)) * kBatch; b < (n + 4 * kBatch - 1) / (4 * kBatch) * (4 * kBatch);
+             b += kThreads / 32 * 4 * kBatch) {
+            float4 x[kBatch][V];
+            bool ok[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int page = b + u < n ? __ldg(row + start + b + u) : -1;
+                ok[u] = (unsigned)page < (unsigned)c.pages;
+                const float4* m = reinterpret_cast<const float4*>(c.mean + ((size_t)(ok[u] ? page : 0) * c.hkv + w.g) * D);
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[u][i] = ok[u] ? __ldg(m + l8 + 8 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int h = 0; h < kRowHeads; ++h) {
+                if (h < w.nh) {
+                    float s[kBatch];
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) s[u] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float4 q4 = qs[h][l8 + 8 * i];
+#pragma unroll
+                        for (int u = 0; u < kBatch; ++u) {
+                            s[u] = fmaf(q4.x, x[u][i].x, s[u]);
+                            s[u] = fmaf(q4.y, x[u][i].y, s[u]);
+                            s[u] = fmaf(q4.z, x[u][i].z, s[u]);
+                            s[u] = fmaf(q4.w, x[u][i].w, s[u]);
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+#pragma unroll
+                        for (int off = 4; off > 0; off >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], off);
+                        // a NaN, and a page that is not there, ranks last
+                        if (l8 == h && b + u < n) score[h][b + u] = ok[u] && s[u] == s[u] ? s[u] : -INFINITY;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (warp < w.nh)
+            for (int j = lane; j < n; j += 32) insert_ordered<K>(val, idx, score[warp][j], start + j);
+    }
+    // warp = head
+    if (warp < w.nh)
+        take_best<K>(val, idx, n_route, [&](int i, float v, int j) {
+            if (lane == 0) {
+                best_v[warp * n_route + i] = v;
+                best_i[warp * n_route + i] = j;
+                if (cs == 1) pick[warp * n_route + i] = j;
+            }
+        });
+    if (cs > 1) {
+        cluster.sync();
+        if (rank == 0 && warp < w.nh) {
+#pragma unroll
+            for (int i = 0; i < K; ++i) {
+                val[i] = -INFINITY;
+                idx[i] = INT_MAX;
+            }
+            for (int i = lane; i < cs * n_route; i += 32) {
+                const int from = i / n_route, at = warp * n_route + i - from * n_route;
+                insert_ordered<K>(val, idx, cluster.map_shared_rank(best_v, from)[at],
+                                  cluster.map_shared_rank(best_i, from)[at]);
+            }
+            take_best<K>(val, idx, n_route, [&](int i, float, int j) {
+                if (lane == 0) pick[warp * n_route + i] = j;
+            });
+        }
+        cluster.sync();  // the lists have been read
+        if (rank) return;
     }
     __syncthreads();
     // union of the heads' choices: a block's first mention leads; it counts the leaders before it
@@ -298,6 +366,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 0) *abort_flag = 0;
+    cudaGridDependencySynchronize();  // the plan is written
 
     // Every CTA adds up the rows' tiles: thread i takes a contiguous part of the rows.
     const int per_thread = (a.rows + kWarps * 32 - 1) / (kWarps * 32);
@@ -712,23 +781,47 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
         }
 }
 
+template <int D, int K>
+cudaError_t launch_plan(const View& c, const DecodeArgs& a, const DecodeWs& ws, int num_sms, cudaStream_t st) {
+    // A CTA scores 64 blocks at a time.  Where a row may have more than two such rounds and the rows
+    // are too few to fill the GPU, eight CTAs share one.
+    const int cs = a.topk > 1 && c.max_blocks > 128 && a.rows * 2 <= num_sms ? 8 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.rows * cs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cs;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_plan_kernel<D, K>, c, a, ws);
+}
+
 template <int D>
 cudaError_t launch_decode_d(const View& c, const DecodeArgs& a, const DecodeWs& ws, int num_sms, cudaStream_t st) {
     const int route = a.topk - 1;
-    if (route <= 4)
-        cache_plan_kernel<D, 4><<<a.rows, kThreads, 0, st>>>(c, a, ws);
-    else if (route <= 8)
-        cache_plan_kernel<D, 8><<<a.rows, kThreads, 0, st>>>(c, a, ws);
-    else if (route <= 16)
-        cache_plan_kernel<D, 16><<<a.rows, kThreads, 0, st>>>(c, a, ws);
-    else
-        cache_plan_kernel<D, 32><<<a.rows, kThreads, 0, st>>>(c, a, ws);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = route <= 4    ? launch_plan<D, 4>(c, a, ws, num_sms, st)
+                    : route <= 8  ? launch_plan<D, 8>(c, a, ws, num_sms, st)
+                    : route <= 16 ? launch_plan<D, 16>(c, a, ws, num_sms, st)
+                                  : launch_plan<D, 32>(c, a, ws, num_sms, st);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    cache_attn_kernel<D><<<min(num_sms, kMaxCtas), kWarps * 32, kSmem, st>>>(c, a, ws);
-    return cudaGetLastError();
+    // Programmatic launch: the attention's CTAs start while the plan runs, and wait for it to end
+    // before they read anything.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(min(num_sms, kMaxCtas));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_attn_kernel<D>, c, a, ws);
 }
 
 }  // namespace

@@ -268,6 +268,43 @@ def test_decode_is_the_model(d, heads, group, chunk, topk, lengths):
     cache_status(c)
 
 
+@pytest.mark.parametrize("blocks,heads,group,topk", [(130, 1, 2, 4), (140, 2, 8, 32), (1300, 1, 1, 9), (9000, 1, 3, 3)])
+def test_gate_over_many_blocks(blocks, heads, group, topk):
+    """Rows of more blocks than one CTA scores in two rounds, than one window, and than a cluster's windows: the
+    choice is the model's.  The pages hold one token's worth of difference: keys and values are the block's own
+    constants, written into the pools directly."""
+    d, chunk = 64, 128
+    n = blocks * chunk - 5
+    gen = torch.Generator().manual_seed(blocks)
+    c = KVCache(blocks, 1, blocks + 3, heads, d, chunk)
+    order = torch.randperm(blocks, generator=gen)
+    c.table[0, :blocks] = order.int().cuda()
+    c.refs.fill_(1)
+    c.lengths.fill_(n)
+    code = torch.randint(0, 256, (blocks, heads, 1, d // 2), generator=gen, dtype=torch.uint8)
+    for x in (c.k_codes, c.v_codes):
+        x.copy_(code.expand(-1, -1, chunk, -1))
+    for x in (c.k_scales, c.v_scales):
+        x.view(torch.uint8).fill_(0x30)  # 0.5
+    held = M.values(unpack(code), np.full((blocks, heads, 1, d // 16), 0x30))[order.numpy(), :, 0]  # by block
+    c.k_mean.copy_(torch.tensor(held[np.argsort(order.numpy())]))
+    q = torch.randn((1, heads * group, d), generator=gen).bfloat16()
+    o, l = cache_decode(c, q.cuda(), topk)
+    cache_status(c)
+    for h in range(heads * group):
+        kb = held[:, h // group]
+        s = kb @ host(q)[0, h]
+        order_h = np.lexsort((np.arange(blocks - 1), -s[:-1]))
+        assert s[order_h[topk - 2]] - s[order_h[topk - 1]] > 2 * (d + 1) * 2.0 ** -24 * 6 * 0.5 * np.abs(host(q)[0, h]).sum()
+        take = list(order_h[:topk - 1]) + [blocks - 1]
+        z = s[take] / 8
+        w = np.exp(z - z.max()) * np.where(np.array(take) == blocks - 1, chunk - 5, chunk)
+        want = w @ kb[take] / w.sum()
+        pv = w @ np.abs(kb[take]) / w.sum()
+        assert (np.abs(host(o)[0, h] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * pv).all()
+        assert abs(host(l)[h, 0] - z.max() - np.log(w.sum())) < 1e-4
+
+
 @pytest.mark.parametrize("topk", [0, 3])
 def test_decode_scales_and_magnitudes(topk):
     """A softmax scale of the caller's, exponents, queries near the ends of bf16's range, heads of zeros."""
