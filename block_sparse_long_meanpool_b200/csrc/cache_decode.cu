@@ -270,10 +270,6 @@ constexpr int kSmem = 232448;  // shared memory of a CTA
 #ifndef CFG_DEPTH
 #define CFG_DEPTH 3
 #endif
-#ifndef CFG_SHORT
-#define CFG_SHORT 16
-#endif
-constexpr int kShortRow = CFG_SHORT;  // rows of fewer tiles than this on average go to single warps
 constexpr float kLag = 8.f;
 
 // A tile in shared memory.
@@ -287,8 +283,8 @@ struct Tile {
 // that layers with few query heads per KV head may get longer rings.
 template <int D>
 struct Smem {
-    static constexpr int kMisc = 0;  // abort flag, last flags, scan
-    static constexpr int kMl = 8 + 4 * kWarps + 24 * kWarps;   // [warps][heads] float2
+    static constexpr int kMisc = 0;  // abort flag, last flag, scan
+    static constexpr int kMl = 8 + 24 * kWarps;   // [warps][heads] float2
     static constexpr int kState = (kMl + kWarps * kRowHeads * 8 + 127) / 128 * 128;  // [warps][row heads][D] fp32
     __host__ __device__ static int ring(int heads) { return kState + kWarps * heads * D * 4; }
     __host__ __device__ static int depth(int heads) {  // tiles of a warp's ring
@@ -357,7 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
     const uint32_t base = ptx::smem_u32(smem);
     volatile int* abort_flag = reinterpret_cast<int*>(smem + S::kMisc);
-    long long* scan = reinterpret_cast<long long*>(smem + S::kMisc + 8 + 4 * kWarps);
+    long long* scan = reinterpret_cast<long long*>(smem + S::kMisc + 8);
     const int depth = S::depth(a.row_heads);  // the warp's ring, its barriers and metas
     const int ring = S::ring(a.row_heads) + warp * depth * T::kBytes;
     const int bars = S::ring(a.row_heads) + kWarps * depth * T::kBytes + warp * depth * 16, metas = bars + 8 * depth;
@@ -387,13 +383,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
         if (i < warp) before += scan[i];
         all_tiles += scan[i];
     }
-    // Rows of few tiles go to single warps, so that no warp waits for its CTA at every row's end.
-    const int tn = all_tiles < (long long)kShortRow * a.rows && a.rows > gridDim.x ? 1 : kWarps;
+    // Where there are more rows than CTAs, a team is one warp, and no warp waits for its CTA at a
+    // row's end; with fewer rows a row has so many parts that CTAs have to merge their own first.
+    const int tn = a.rows > gridDim.x ? 1 : kWarps;
     const int tw = tn == 1 ? 0 : warp, team = tn == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
-    const int members = tn * 32, me = tn == 1 ? lane : tid;
-    // teams that work: a tile at least for each warp where there are that few
-    const long long teams = max(1LL, min((long long)gridDim.x * (kWarps / tn), (all_tiles + tn - 1) / tn));
-    const long long share = all_tiles / teams, extra = all_tiles - share * teams;  // the first `extra` have one more
+    const int me = tn == 1 ? lane : tid;
+    // Teams that work: a tile at least for each warp where there are that few.  The first `extra`
+    // have one tile more than the others.
+    const long long room = (long long)gridDim.x * (kWarps / tn), wanted = (all_tiles + tn - 1) / tn;
+    const unsigned teams = (unsigned)max(1LL, min(room, wanted));
+    const long long share = all_tiles >> 32 ? all_tiles / teams : (unsigned)all_tiles / teams;
+    const long long extra = all_tiles - share * teams;
     const long long begin = team * share + min((long long)team, extra), end = begin + share + (team < extra);
     // the thread that holds a team's first tile's row finds it
     __syncthreads();
@@ -411,10 +411,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
     }
     __syncthreads();
     if (team >= teams || begin >= end) return;
-    auto sync_team = [&]() {
-        if (tn == 1) __syncwarp();
-        else __syncthreads();
-    };
     const int total = (int)(end - begin);
     Segment seg;
     seg.row = (int)scan[kWarps + (tn == 1 ? 2 * warp : 0)];
@@ -449,20 +445,23 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
             while (next >= ahead.at + ahead.n);
             own_tile = -1;
         }
-        if (own_tile < 0) {
-            const Row w = row_of(c, a, ahead.row);
-            own_len = (held_tokens(c, w.seq) - 1) % c.chunk + 1;
-            own_tile = ahead.row_n - (own_len + kTile - 1) / kTile;
-            all_heads = (1 << w.nh) - 1;
-            list = a.topk ? ws.items + (size_t)ahead.row * a.max_items
-                          : reinterpret_cast<const int2*>(c.table + (size_t)w.seq * c.max_blocks);
-            code_at = (size_t)w.g * c.chunk * (D / 2);
-        }
         const int tile = ahead.t0 + next - ahead.at;
         int block = __umulhi(tile, inv_block);
         sub = tile - block * per_block;
         if (sub < 0) --block, sub += per_block;
+        if (own_tile < 0) {
+            const Row w = row_of(c, a, ahead.row);
+            list = a.topk ? ws.items + (size_t)ahead.row * a.max_items
+                          : reinterpret_cast<const int2*>(c.table + (size_t)w.seq * c.max_blocks);
+            all_heads = (1 << w.nh) - 1;
+            code_at = (size_t)w.g * c.chunk * (D / 2);
+            own_len = __ldg(c.lengths + w.seq);
+        }
         item = a.topk ? __ldcg(list + block) : make_int2(__ldg(reinterpret_cast<const int*>(list) + block), all_heads);
+        if (own_tile < 0) {
+            own_len = (own_len - 1) % c.chunk + 1;
+            own_tile = ahead.row_n - (own_len + kTile - 1) / kTile;
+        }
         valid = tile >= own_tile ? min(kTile, own_len - sub * kTile) : kTile;
     };
     auto fetch = [&]() {
@@ -690,85 +689,156 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
                 l0 += __shfl_xor_sync(0xffffffffu, l0, off);
                 l1 += __shfl_xor_sync(0xffffffffu, l1, off);
             }
-            if (g8 == 0) {
-                ml[warp * kRowHeads + 2 * t4] = make_float2(m0, l0);
-                ml[warp * kRowHeads + 2 * t4 + 1] = make_float2(m1, l1);
-            }
-            float* mine_o = state + (warp * a.row_heads + 2 * t4) * D + g8 * (D / 8);
-#pragma unroll
-            for (int i = 0; i < kMt; ++i) {
-                if (2 * t4 < w.nh) *reinterpret_cast<float2*>(mine_o + 2 * i) = make_float2(o[i][0], o[i][2]);
-                if (2 * t4 + 1 < w.nh) *reinterpret_cast<float2*>(mine_o + D + 2 * i) = make_float2(o[i][1], o[i][3]);
-            }
         }
-        sync_team();
-        // The team's: the warps that took tiles are those of the segment's first tn tiles.
-        const int parts = min(seg.n, tn), first = tn == 1 ? warp : seg.at % tn;
         const bool whole = seg.n == seg.row_n;
         const int part = 2 * team + (seg.at > 0);
-        for (int i = me; i < w.nh * D; i += members) {
-            const int h = i / D, e = i - h * D;
-            float m = -INFINITY;
-            for (int k = 0, j = first; k < parts; ++k, j = j + 1 == tn ? 0 : j + 1) m = fmaxf(m, ml[j * kRowHeads + h].x);
-            const float ref = m == -INFINITY ? 0.f : m;
-            float l = 0.f, acc = 0.f;
-            for (int k = 0, j = first; k < parts; ++k, j = j + 1 == tn ? 0 : j + 1) {
-                const float2 x = ml[j * kRowHeads + h];
-                const float f = ptx::ex2(x.x - ref);
-                l = fmaf(f, x.y, l);
-                acc = fmaf(f, state[(j * a.row_heads + h) * D + e], acc);
-            }
-            if (whole) {
-                a.out[((size_t)w.seq * a.hq + w.h0 + h) * D + e] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l * c.v_unit);
-                if (e == 0) a.lse[(size_t)(w.h0 + h) * c.seqs + w.seq] = m * 0.69314718055994531f + logf(l);
-            } else {
-                ws.part_o[((size_t)part * a.row_heads + h) * D + e] = acc;
-                if (e == 0) ws.part_ml[part * a.row_heads + h] = make_float2(m, l);
-            }
-        }
+        __nv_bfloat16* out = a.out + ((size_t)w.seq * a.hq + w.h0) * D;
+        float* lse = a.lse + (size_t)w.h0 * c.seqs + w.seq;
+        // Parts of a row come from the teams that hold its first to last tile; the last team to
+        // write its part adds all of them, in order, so that the sums do not depend on timing.
+        // Only the first part can begin behind its team's first tile (the team's second part).
+        int c0 = 0, c1 = 0, skew = 0;
         if (!whole) {
-            // Parts come from the teams that hold the row's first to last tile; the last team to write
-            // its part adds all of them in order.
             auto holder = [&](long long tile) {
                 const long long longer = extra * (share + 1);
                 return (int)(tile < longer ? tile / (share + 1) : extra + (tile - longer) / share);
             };
-            const int c0 = holder(row_start), c1 = holder(row_start + seg.row_n - 1);
-            int* last = reinterpret_cast<int*>(smem + S::kMisc + 8) + (tn == 1 ? warp : 0);
-            __threadfence();
-            sync_team();
-            if (me == 0) *last = atomicAdd(ws.done + seg.row, 1) == c1 - c0;
-            sync_team();
-            if (*last) {
-                __threadfence();
-                // only the first part can begin behind its team's first tile (the second slot)
-                const int skew = row_start > c0 * share + min((long long)c0, extra);
-                for (int i = me; i < w.nh * D; i += members) {
-                    const int h = i / D, e = i - h * D;
-                    float m = -INFINITY;
-#pragma unroll 8
-                    for (int k = c0; k <= c1; ++k)
-                        m = fmaxf(m, __ldcg(ws.part_ml + (2 * k + (k == c0 ? skew : 0)) * a.row_heads + h).x);
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    float l = 0.f, acc = 0.f;
-#pragma unroll 8
-                    for (int k = c0; k <= c1; ++k) {
-                        const size_t sl = (size_t)(2 * k + (k == c0 ? skew : 0)) * a.row_heads + h;
-                        const float2 x = __ldcg(ws.part_ml + sl);
-                        const float f = ptx::ex2(x.x - ref);
-                        l = fmaf(f, x.y, l);
-                        acc = fmaf(f, __ldcg(ws.part_o + sl * D + e), acc);
+            c0 = holder(row_start);
+            c1 = holder(row_start + seg.row_n - 1);
+            skew = row_start > c0 * share + min((long long)c0, extra);
+        }
+        // four channels' sum of parts k0, k0 + step, ...
+        auto gather = [&](int h, int e, int k0, int step, float& m, float& l, float4& acc) {
+            m = -INFINITY, l = 0.f, acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int k = k0; k <= c1; k += step) {
+                const size_t at = (size_t)(2 * k + (k == c0 ? skew : 0)) * a.row_heads + h;
+                const float2 x = __ldcg(ws.part_ml + at);
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(ws.part_o + at * D) + e);
+                const float n = fmaxf(m, x.x), ref = n == -INFINITY ? 0.f : n;
+                const float f = ptx::ex2(m - ref), f2 = ptx::ex2(x.x - ref);
+                m = n;
+                l = l * f + x.y * f2;
+                acc = make_float4(acc.x * f + v.x * f2, acc.y * f + v.y * f2, acc.z * f + v.z * f2, acc.w * f + v.w * f2);
+            }
+        };
+        auto write = [&](int h, int e, float m, float l, const float4& acc) {
+            const float f = l == 0.f ? 0.f : c.v_unit / l;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f), hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+            *reinterpret_cast<uint2*>(out + h * D + 4 * e) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            if (e == 0) lse[(size_t)h * c.seqs] = m * 0.69314718055994531f + logf(l);
+        };
+        if (tn == 1) {
+            // this thread's channels g8 * (D / 8) .. of heads 2 t4 and 2 t4 + 1
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int h = 2 * t4 + k;
+                const float m = k ? m1 : m0, l = k ? l1 : l0;
+                if (h < w.nh) {
+#pragma unroll
+                    for (int i = 0; i < kMt; i += 2) {
+                        const int e = g8 * (D / 32) + i / 2;
+                        const float4 v = make_float4(o[i][k], o[i][2 + k], o[i + 1][k], o[i + 1][2 + k]);
+                        if (whole)
+                            write(h, e, m, l, v);
+                        else
+                            __stcg(reinterpret_cast<float4*>(ws.part_o + ((size_t)part * a.row_heads + h) * D) + e, v);
                     }
-                    a.out[((size_t)w.seq * a.hq + w.h0 + h) * D + e] =
-                        __float2bfloat16_rn(l == 0.f ? 0.f : acc / l * c.v_unit);
-                    if (e == 0) a.lse[(size_t)(w.h0 + h) * c.seqs + w.seq] = m * 0.69314718055994531f + logf(l);
+                    if (!whole && g8 == 0) __stcg(ws.part_ml + (size_t)part * a.row_heads + h, make_float2(m, l));
+                }
+            }
+            if (!whole) {
+                __threadfence();
+                __syncwarp();
+                int last = 0;
+                if (lane == 0) last = atomicAdd(ws.done + seg.row, 1) == c1 - c0;
+                if (__shfl_sync(0xffffffffu, last, 0)) {
+                    __threadfence();
+                    for (int i = lane; i < w.nh * (D / 4); i += 32) {
+                        const int h = i / (D / 4), e = i - h * (D / 4);
+                        float m, l;
+                        float4 acc;
+                        gather(h, e, c0, 1, m, l, acc);
+                        write(h, e, m, l, acc);
+                    }
+                }
+            }
+        } else {
+            if (takes) {
+                if (g8 == 0) {
+                    ml[warp * kRowHeads + 2 * t4] = make_float2(m0, l0);
+                    ml[warp * kRowHeads + 2 * t4 + 1] = make_float2(m1, l1);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < kMt; i += 2)
+                        if (2 * t4 + k < w.nh)
+                            *reinterpret_cast<float4*>(state + (warp * a.row_heads + 2 * t4 + k) * D + g8 * (D / 8) + 2 * i) =
+                                make_float4(o[i][k], o[i][2 + k], o[i + 1][k], o[i + 1][2 + k]);
+            }
+            __syncthreads();
+            // the sum of n states from `first` on, for four channels
+            auto collect = [&](int h, int e, int first, int n, float& m, float& l, float4& acc) {
+                m = -INFINITY;
+                for (int k = 0, j = first; k < n; ++k, j = j + 1 == kWarps ? 0 : j + 1) m = fmaxf(m, ml[j * kRowHeads + h].x);
+                const float ref = m == -INFINITY ? 0.f : m;
+                l = 0.f, acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0, j = first; k < n; ++k, j = j + 1 == kWarps ? 0 : j + 1) {
+                    const float2 x = ml[j * kRowHeads + h];
+                    const float4 v = *reinterpret_cast<const float4*>(state + (j * a.row_heads + h) * D + 4 * e);
+                    const float f = ptx::ex2(x.x - ref);
+                    l = fmaf(f, x.y, l);
+                    acc = make_float4(fmaf(f, v.x, acc.x), fmaf(f, v.y, acc.y), fmaf(f, v.z, acc.z), fmaf(f, v.w, acc.w));
+                }
+            };
+            // the warps that took tiles are those of the segment's first tiles
+            for (int i = tid; i < w.nh * (D / 4); i += kWarps * 32) {
+                const int h = i / (D / 4), e = i - h * (D / 4);
+                float m, l;
+                float4 acc;
+                collect(h, e, seg.at % kWarps, min(seg.n, kWarps), m, l, acc);
+                if (whole) {
+                    write(h, e, m, l, acc);
+                } else {
+                    __stcg(reinterpret_cast<float4*>(ws.part_o + ((size_t)part * a.row_heads + h) * D) + e, acc);
+                    if (e == 0) __stcg(ws.part_ml + (size_t)part * a.row_heads + h, make_float2(m, l));
+                }
+            }
+            if (!whole) {
+                volatile int* last = reinterpret_cast<int*>(smem + S::kMisc + 4);
+                __threadfence();
+                __syncthreads();
+                if (tid == 0) *last = atomicAdd(ws.done + seg.row, 1) == c1 - c0;
+                __syncthreads();
+                if (*last) {
+                    // groups of threads add every groups-th part, then their sums are added
+                    __threadfence();
+                    const int quads = w.nh * (D / 4), groups = min(kWarps, max(1, kWarps * 32 / quads));
+                    for (int i = tid; i < groups * quads; i += kWarps * 32) {
+                        const int group = i / quads, x = i - group * quads, h = x / (D / 4), e = x - h * (D / 4);
+                        float m, l;
+                        float4 acc;
+                        gather(h, e, c0 + group, groups, m, l, acc);
+                        *reinterpret_cast<float4*>(state + (group * a.row_heads + h) * D + 4 * e) = acc;
+                        if (e == 0) ml[group * kRowHeads + h] = make_float2(m, l);
+                    }
+                    __syncthreads();
+                    for (int i = tid; i < quads; i += kWarps * 32) {
+                        const int h = i / (D / 4), e = i - h * (D / 4);
+                        float m, l;
+                        float4 acc;
+                        collect(h, e, 0, groups, m, l, acc);
+                        write(h, e, m, l, acc);
+                    }
                 }
             }
         }
         if (seg.at + seg.n >= total) break;
         row_start += seg.t0 + seg.n;  // a segment that another follows ends its row
         next_segment(seg, ws.tiles, total);
-        sync_team();  // the state is free again
+        if (tn != 1) __syncthreads();  // the state is free again
     }
     // After a wait that gave up, the copies still in flight land before the memory is given back.
     if (next == INT_MAX)

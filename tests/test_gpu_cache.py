@@ -268,6 +268,21 @@ def test_decode_is_the_model(d, heads, group, chunk, topk, lengths):
     cache_status(c)
 
 
+@pytest.mark.parametrize("d,heads,group,topk,longest", [(64, 1, 1, 0, 300), (128, 1, 3, 2, 700), (64, 2, 9, 0, 260),
+                                                         (128, 1, 8, 3, 500)])
+def test_decode_of_more_rows_than_multiprocessors(d, heads, group, topk, longest):
+    """Many short rows, which single warps take: whole rows, rows cut between two warps, empty slots."""
+    rng = np.random.default_rng(25)
+    seqs, chunk = 170, 128
+    lengths = rng.integers(0, 60, seqs)
+    lengths[rng.permutation(seqs)[:30]] = rng.integers(100, longest, 30)
+    lengths[::11] = 0
+    c, m = pair(sum(-(-int(n) // chunk) for n in lengths), seqs, -(-longest // chunk), heads, d, chunk)
+    fill(c, m, rng, lengths)
+    check_decode(c, m, rng.standard_normal((seqs, heads * group, d)), topk)
+    cache_status(c)
+
+
 @pytest.mark.parametrize("blocks,heads,group,topk", [(130, 1, 2, 4), (140, 2, 8, 32), (1300, 1, 1, 9), (9000, 1, 3, 3)])
 def test_gate_over_many_blocks(blocks, heads, group, topk):
     """Rows of more blocks than one CTA scores in two rounds, than one window, and than a cluster's windows: the
