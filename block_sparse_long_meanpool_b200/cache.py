@@ -24,7 +24,8 @@ from .moba import MobaCache, MobaError, _check, load_library
 
 GROUP = 16  # channels per scale
 
-_POOLS = ("k_codes", "k_scales", "v_codes", "v_scales")
+# the current stream's handle, without making a Stream object of it
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _fail(msg):
@@ -129,7 +130,7 @@ def _call(c, fn, *args):
     if torch.cuda.current_device() != index:  # the launch takes the current device
         with torch.cuda.device(index):
             return _call(c, fn, *args)
-    status = fn(c._ref, *args, torch.cuda.current_stream(index).cuda_stream)
+    status = fn(c._ref, *args, _raw_stream(index))
     if status:
         _check(status)
 

@@ -1,4 +1,5 @@
 // Host side of the paged 4-bit cache (include/moba.h): argument checks, workspace layout, launches.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -110,10 +111,14 @@ cache::View view(const moba_cache& c) {
     return v;
 }
 
+// Multiprocessors of the current device, asked for once per device.
 int device_sm_count() {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

@@ -6,7 +6,7 @@
 // nearest with ties to even; the held value is c s.  Six is the largest e2m1 magnitude, so the
 // group's maximum lands on the last step of the grid.  Streaming: 4 bytes are read per key and
 // value channel pair and 1.125 written.
-//   append_kernel        one CTA per (64-position segment of a sequence's new tokens, KV head)
+//   append_kernel        one CTA per (64-position segment of a sequence's new tokens, some KV heads)
 //   append_means_kernel  one CTA per (completed block, KV head), and one warp per sequence that
 //                        moves its length
 #include "cache_internal.cuh"
@@ -122,10 +122,11 @@ __device__ __forceinline__ void held_f16(uint2 codes, uint32_t scale, uint32_t (
 
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-append_kernel(View c, AppendArgs a) {
+append_kernel(View c, AppendArgs a, int heads) {
     constexpr int kPerTok = D / kGroup;  // groups of a token
     __shared__ int s_page, s_off, s_cnt, s_row;
-    const int g = blockIdx.y;
+    cudaTriggerProgrammaticLaunchCompletion();
+    const int g0 = blockIdx.y * heads, ng = min(heads, c.hkv - g0);
     if (threadIdx.x < 32) {
         NewTokens t;
         int u;
@@ -147,20 +148,23 @@ append_kernel(View c, AppendArgs a) {
     __syncthreads();
     const int cnt = s_cnt;
     if (cnt == 0) return;
-    const size_t crow = code_row(c, s_page, g), srow = scale_row(c, s_page, g);
-    for (int i = threadIdx.x; i < 2 * cnt * kPerTok; i += kThreads) {
-        const bool is_v = i >= cnt * kPerTok;
-        const int e = is_v ? i - cnt * kPerTok : i;
+    const size_t crow = code_row(c, s_page, g0), srow = scale_row(c, s_page, g0);
+    const int per_head = cnt * kPerTok, per_kv = ng * per_head;
+    for (int i = threadIdx.x; i < 2 * per_kv; i += kThreads) {
+        const bool is_v = i >= per_kv;
+        int e = is_v ? i - per_kv : i;
+        const int g = cnt == kSeg ? e / (kSeg * kPerTok) : e / per_head;  // a shift for whole segments
+        e -= g * per_head;
         const int tok = e / kPerTok, grp = e - tok * kPerTok;
-        const size_t src = ((size_t)(s_row + tok) * c.hkv + g) * D + grp * kGroup;
+        const size_t src = ((size_t)(s_row + tok) * c.hkv + g0 + g) * D + grp * kGroup;
         const uint4* x = reinterpret_cast<const uint4*>((is_v ? a.v : a.k) + src);
         const uint4 x0 = __ldcs(x), x1 = __ldcs(x + 1);
         const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
         const float unit = is_v ? c.v_unit : c.k_unit;
         const Quantised r = quantise(w, 1.f / unit);  // a power of two
-        const int at = s_off + tok;
-        *reinterpret_cast<uint2*>((is_v ? c.vc : c.kc) + crow + (size_t)at * (D / 2) + grp * 8) = r.codes;
-        ((is_v ? c.vs : c.ks) + srow)[(size_t)at * kPerTok + grp] = (uint8_t)r.scale;
+        const size_t at = (size_t)g * c.chunk + s_off + tok;
+        *reinterpret_cast<uint2*>((is_v ? c.vc : c.kc) + crow + at * (D / 2) + grp * 8) = r.codes;
+        ((is_v ? c.vs : c.ks) + srow)[at * kPerTok + grp] = (uint8_t)r.scale;
         if (a.k_held) {
             uint32_t h[8], o[8];
             held_f16(r.codes, r.scale, h);
@@ -189,6 +193,7 @@ append_means_kernel(View c, AppendArgs a, int blocks) {
     __shared__ int s_page;
     const int tid = threadIdx.x, lane = tid & 31, g = blockIdx.y;
     if (blockIdx.x >= blocks) {
+        cudaGridDependencySynchronize();  // the kernel before this one reads the lengths
         const int i = (blockIdx.x - blocks) * (kThreads / 32) + (tid >> 5);
         if (g || i >= c.seqs) return;
         bool bad;
@@ -216,21 +221,34 @@ append_means_kernel(View c, AppendArgs a, int blocks) {
     }
     __syncthreads();
     if (s_page < 0) return;
+    cudaGridDependencySynchronize();
     const uint8_t* codes = c.kc + code_row(c, s_page, g);
     const uint8_t* scales = c.ks + scale_row(c, s_page, g);
     const int row = tid / kPerTok, grp = tid - row * kPerTok;
     float acc[kGroup];
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) acc[i] = 0.f;
-    for (int r = row; r < c.chunk; r += kRows) {
-        const uint2 w = *reinterpret_cast<const uint2*>(codes + (size_t)r * (D / 2) + grp * 8);
-        uint32_t h[8];
-        held_f16(w, scales[(size_t)r * kPerTok + grp], h);
+    // kAhead rows are read before the first is added; those behind the block add zeros
+    constexpr int kAhead = 8;
+    for (int r = row; r < c.chunk; r += kRows * kAhead) {
+        uint2 w[kAhead];
+        uint32_t sc[kAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 f = f16x2_to_f32(h[i]);
-            acc[2 * i] += f.x;
-            acc[2 * i + 1] += f.y;
+        for (int j = 0; j < kAhead; ++j) {
+            const int at = r + j * kRows;
+            w[j] = at < c.chunk ? *reinterpret_cast<const uint2*>(codes + (size_t)at * (D / 2) + grp * 8) : make_uint2(0, 0);
+            sc[j] = at < c.chunk ? scales[(size_t)at * kPerTok + grp] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            uint32_t h[8];
+            held_f16(w[j], sc[j], h);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = f16x2_to_f32(h[i]);
+                acc[2 * i] += f.x;
+                acc[2 * i + 1] += f.y;
+            }
         }
     }
 #pragma unroll
@@ -250,12 +268,14 @@ cudaError_t launch_append_d(const View& c, const AppendArgs& a, cudaStream_t st)
     const long long n = a.total;
     const long long segs = min(n, n / kSeg + 2LL * c.seqs);
     const long long blocks = min(n, n / c.chunk + c.seqs);
-    append_kernel<D><<<dim3((unsigned)segs, c.hkv), kThreads, 0, st>>>(c, a);
+    // A CTA takes as many KV heads as leave about eight CTAs to each of the 148 multiprocessors: its
+    // search for the segment (three dependent loads) is paid once for them.
+    const int heads = (int)min((long long)c.hkv, max(1LL, segs * c.hkv / 1184));
+    append_kernel<D><<<dim3((unsigned)segs, (c.hkv + heads - 1) / heads), kThreads, 0, st>>>(c, a, heads);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int movers = (c.seqs + kThreads / 32 - 1) / (kThreads / 32);
-    append_means_kernel<D><<<dim3((unsigned)(blocks + movers), c.hkv), kThreads, 0, st>>>(c, a, (int)blocks);
-    return cudaGetLastError();
+    return launch_early(append_means_kernel<D>, dim3((unsigned)(blocks + movers), c.hkv), kThreads, 0, st, c, a, (int)blocks);
 }
 
 }  // namespace

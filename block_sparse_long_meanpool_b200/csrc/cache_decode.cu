@@ -8,6 +8,7 @@
 //   cache_plan_kernel  one CTA per row: gate scores, the heads' choices, their union
 //   cache_attn_kernel  as many CTAs as fit the GPU at once, each with an equal share of all rows'
 //                      64-token tiles; a row that several CTAs share is merged by the last of them
+#include <atomic>
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -388,37 +389,77 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
     const int tn = a.rows > gridDim.x ? 1 : kWarps;
     const int tw = tn == 1 ? 0 : warp, team = tn == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
     const int me = tn == 1 ? lane : tid;
-    // Teams that work: a tile at least for each warp where there are that few.  The first `extra`
-    // have one tile more than the others.
-    const long long room = (long long)gridDim.x * (kWarps / tn), wanted = (all_tiles + tn - 1) / tn;
-    const unsigned teams = (unsigned)max(1LL, min(room, wanted));
-    const long long share = all_tiles >> 32 ? all_tiles / teams : (unsigned)all_tiles / teams;
-    const long long extra = all_tiles - share * teams;
-    const long long begin = team * share + min((long long)team, extra), end = begin + share + (team < extra);
-    // the thread that holds a team's first tile's row finds it
-    __syncthreads();
-    if (me == 0) scan[tn == 1 ? warp : 0] = team < teams && begin < end ? begin : -1;
-    __syncthreads();
-    for (int i = 0; i < kWarps / tn; ++i) {
-        const long long b = scan[i];
-        if (before <= b && b < before + mine) {
-            long long at = before;
-            int r = r0;
-            for (int n; at + (n = __ldcg(ws.tiles + r)) <= b; ++r) at += n;
-            scan[kWarps + 2 * i] = r;
-            scan[kWarps + 2 * i + 1] = at;
-        }
-    }
-    __syncthreads();
-    if (team >= teams || begin >= end) return;
-    const int total = (int)(end - begin);
     Segment seg;
-    seg.row = (int)scan[kWarps + (tn == 1 ? 2 * warp : 0)];
-    long long row_start = scan[kWarps + (tn == 1 ? 2 * warp + 1 : 1)];  // first tile of seg's row among all tiles
     seg.at = 0;
-    seg.t0 = (int)(begin - row_start);
-    seg.row_n = __ldcg(ws.tiles + seg.row);
-    seg.n = min(seg.row_n - seg.t0, total);
+    int total;               // the team's tiles
+    long long row_start = 0;  // first tile of seg's row among all tiles
+    long long share = 0, extra = 0;  // tiles of a team: share, one more for the first `extra` teams
+    int first_team = -1, row_teams = 0;  // where every team keeps to one row: the row's teams
+    // A CTA that passes from one row to the next merges and starts twice, which costs about nine
+    // tiles' time.  Where that is more than what keeping to one row costs (a row's CTAs are a whole
+    // number, so the fullest has up to rows / (CTAs - rows) more tiles than the average), it does.
+    const int spare = (int)gridDim.x - a.rows;
+    if (spare > 0 && all_tiles * a.rows < 9LL * gridDim.x * spare) {
+        const int most = max((int)((unsigned)all_tiles + spare - 1) / spare, kWarps);  // tiles of a CTA
+        const int n = r0 < r1 ? ((int)mine + most - 1) / most : 0;  // CTAs of this thread's row (rows < threads)
+        int upto = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = upto;
+        if (tid == 0) scan[kWarps] = -1;
+        __syncthreads();
+        for (int i = 0; i < warp; ++i) upto += (int)scan[i];
+        if (blockIdx.x < upto && blockIdx.x >= upto - n) {
+            scan[kWarps + 1] = upto - n;
+            scan[kWarps + 2] = n;
+            scan[kWarps + 3] = mine;
+            scan[kWarps] = r0;
+        }
+        __syncthreads();
+        if (scan[kWarps] < 0) return;
+        seg.row = (int)scan[kWarps];
+        first_team = (int)scan[kWarps + 1];
+        row_teams = (int)scan[kWarps + 2];
+        seg.row_n = (int)scan[kWarps + 3];
+        const int q = seg.row_n / row_teams, rem = seg.row_n - q * row_teams, j = blockIdx.x - first_team;
+        seg.t0 = j * q + min(j, rem);
+        seg.n = total = q + (j < rem);
+    } else {
+        // Teams that work: a tile at least for each warp where there are that few, but a team for each
+        // row where that is more.
+        const long long room = (long long)gridDim.x * (kWarps / tn);
+        const long long wanted = max((all_tiles + tn - 1) / tn, min((long long)a.rows, all_tiles));
+        const unsigned teams = (unsigned)max(1LL, min(room, wanted));
+        share = all_tiles >> 32 ? all_tiles / teams : (unsigned)all_tiles / teams;
+        extra = all_tiles - share * teams;
+        const long long begin = team * share + min((long long)team, extra), end = begin + share + (team < extra);
+        // the thread that holds a team's first tile's row finds it
+        __syncthreads();
+        if (me == 0) scan[tn == 1 ? warp : 0] = team < teams && begin < end ? begin : -1;
+        __syncthreads();
+        for (int i = 0; i < kWarps / tn; ++i) {
+            const long long b = scan[i];
+            if (before <= b && b < before + mine) {
+                long long at = before;
+                int r = r0;
+                for (int n; at + (n = __ldcg(ws.tiles + r)) <= b; ++r) at += n;
+                scan[kWarps + 2 * i] = r;
+                scan[kWarps + 2 * i + 1] = at;
+            }
+        }
+        __syncthreads();
+        if (team >= teams || begin >= end) return;
+        total = (int)(end - begin);
+        seg.row = (int)scan[kWarps + (tn == 1 ? 2 * warp : 0)];
+        row_start = scan[kWarps + (tn == 1 ? 2 * warp + 1 : 1)];
+        seg.t0 = (int)(begin - row_start);
+        seg.row_n = __ldcg(ws.tiles + seg.row);
+        seg.n = min(seg.row_n - seg.t0, total);
+    }
 
     // The warp's tiles go round its ring, fetched on a cursor of its own; a tile's page is looked up
     // when the tile before it is fetched.
@@ -553,19 +594,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
 #pragma unroll
                     for (int mt = 0; mt < kTile / 16; ++mt) {
                         s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
-                        uint32_t x[2][kKw], sc[2][2];
+                        uint32_t x[2][kKw], sc[2];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int key = mt * 16 + 8 * h + kr;
                             lds<kKw>(x[h], src + key * (D / 2) + t4 * (D / 8));
-                            if constexpr (D == 128) {
-                                const uint32_t two = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(src + T::kKs + key * 8 + 2 * t4));
-                                sc[h][0] = __byte_perm(two, 0, 0x1010);
-                                sc[h][1] = __byte_perm(two, 0, 0x3232);
-                            } else {
-                                const uint32_t one = src[T::kKs + key * 4 + t4];
-                                sc[h][0] = sc[h][1] = e4m3x2_to_f16x2(one | one << 8);
-                            }
+                            if constexpr (D == 128)
+                                sc[h] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(src + T::kKs + key * 8 + 2 * t4));
+                            else
+                                sc[h] = e4m3x2_to_f16x2(src[T::kKs + key * 4 + t4]);
                         }
 #pragma unroll
                         for (int i = 0; i < kKw; ++i) {
@@ -574,8 +611,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
                             e2m1x8_to_f16x2(x[1][i], hi);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                lo[j] = hmul2(lo[j], sc[0][i / 2]);
-                                hi[j] = hmul2(hi[j], sc[1][i / 2]);
+                                lo[j] = i < 2 ? hmul2_low(lo[j], sc[0]) : hmul2_high(lo[j], sc[0]);
+                                hi[j] = i < 2 ? hmul2_low(hi[j], sc[1]) : hmul2_high(hi[j], sc[1]);
                             }
                             mma16816(s[mt], lo[0], hi[0], lo[1], hi[1], qf[4 * i], qf[4 * i + 1]);
                             mma16816(s[mt], lo[2], hi[2], lo[3], hi[3], qf[4 * i + 2], qf[4 * i + 3]);
@@ -652,7 +689,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
                             const int group = D == 128 ? g8 : g8 >> 1;
                             const uint32_t sa = src[T::kVs + ka * (D / kGroup) + group];
                             const uint32_t sb = src[T::kVs + kb * (D / kGroup) + group];
-                            sc[h] = e4m3x2_to_f16x2(sa | sb << 8);
+                            sc[h] = e4m3x2_to_f16x2(__byte_perm(sa, sb, 0x0040));
                         }
 #pragma unroll
                         for (int i = 0; i < kVw; ++i) {
@@ -698,7 +735,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
         // write its part adds all of them, in order, so that the sums do not depend on timing.
         // Only the first part can begin behind its team's first tile (the team's second part).
         int c0 = 0, c1 = 0, skew = 0;
-        if (!whole) {
+        if (row_teams) {
+            c0 = first_team;
+            c1 = first_team + row_teams - 1;
+        } else if (!whole) {
             auto holder = [&](long long tile) {
                 const long long longer = extra * (share + 1);
                 return (int)(tile < longer ? tile / (share + 1) : extra + (tile - longer) / share);
@@ -856,6 +896,10 @@ cudaError_t launch_plan(const View& c, const DecodeArgs& a, const DecodeWs& ws, 
     // A CTA scores 64 blocks at a time.  Where a row may have more than two such rounds and the rows
     // are too few to fill the GPU, eight CTAs share one.
     const int cs = a.topk > 1 && c.max_blocks > 128 && a.rows * 2 <= num_sms ? 8 : 1;
+    if (cs == 1) {
+        cache_plan_kernel<D, K><<<a.rows, kThreads, 0, st>>>(c, a, ws);
+        return cudaGetLastError();
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.rows * cs);
     cfg.blockDim = dim3(kThreads);
@@ -877,21 +921,17 @@ cudaError_t launch_decode_d(const View& c, const DecodeArgs& a, const DecodeWs& 
                     : route <= 16 ? launch_plan<D, 16>(c, a, ws, num_sms, st)
                                   : launch_plan<D, 32>(c, a, ws, num_sms, st);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    // the attribute is the device's, and set once for each
+    static std::atomic<bool> set[64];
+    int dev = 0;
+    e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    // Programmatic launch: the attention's CTAs start while the plan runs, and wait for it to end
-    // before they read anything.
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(min(num_sms, kMaxCtas));
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_attn_kernel<D>, c, a, ws);
+    if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
+    }
+    return launch_early(cache_attn_kernel<D>, dim3(min(num_sms, kMaxCtas)), kWarps * 32, kSmem, st, c, a, ws);
 }
 
 }  // namespace

@@ -54,6 +54,15 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
+// Both halves by b's low or high half.
+__device__ __forceinline__ uint32_t hmul2_low(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), __low2half2(*reinterpret_cast<__half2*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmul2_high(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), __high2half2(*reinterpret_cast<__half2*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
     return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
@@ -80,6 +89,23 @@ __device__ __forceinline__ NewTokens new_tokens(const View& c, const int* __rest
     }
     *bad = wrong;
     return t;
+}
+
+// Launches a kernel that may start while the kernel before it in the stream still runs; it calls
+// cudaGridDependencySynchronize before it reads what that one writes, or writes anything.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // ---------------------------------------------------------------------------------------

@@ -127,7 +127,8 @@ fork_plan_kernel(View c, const int* __restrict__ src, const int* __restrict__ ds
     __shared__ unsigned named[65536 / 32];
     __shared__ int s_bad;
     int *len = ws + kLists, *copy = len + n, *list = copy + n;
-    for (int i = threadIdx.x; i < 65536 / 32; i += kPlan) named[i] = 0;
+    cudaTriggerProgrammaticLaunchCompletion();
+    for (int i = threadIdx.x; i < (c.seqs + 31) / 32; i += kPlan) named[i] = 0;
     if (threadIdx.x == 0) s_bad = 0;
     __syncthreads();
     int copies = 0;
@@ -178,30 +179,55 @@ fork_plan_kernel(View c, const int* __restrict__ src, const int* __restrict__ ds
     }
 }
 
-// Copies n bytes (a multiple of 4; 16-byte aligned ends first) with this CTA's threads.
-__device__ __forceinline__ void copy_bytes(uint8_t* dst, const uint8_t* src, size_t n) {
-    const size_t v = n / 16;
-    for (size_t i = threadIdx.x; i < v; i += kThreads)
-        reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
-    for (size_t i = v * 16 + 4 * threadIdx.x; i < n; i += 4 * kThreads)
-        *reinterpret_cast<uint32_t*>(dst + i) = *reinterpret_cast<const uint32_t*>(src + i);
-}
-
-// Tokens [t0, t1) of head g of one page to another, t0 a multiple of kCopyTokens.
+// Tokens [t0, t1) of head g of one page to another, t0 a multiple of kCopyTokens: codes and scales
+// of keys and values.  A thread has kAhead 16-byte loads in flight before it stores; a token's
+// scales are 4 or 8 bytes, so a last piece of up to 12 bytes is copied by words.
 __device__ __forceinline__ void copy_tokens(const View& to, int q, const View& from, int p, int g, int t0, int t1) {
-    const size_t cb = from.d / 2, sb = from.d / kGroup, n = t1 - t0;
-    const size_t c0 = t0 * cb, s0 = t0 * sb;
-    copy_bytes(to.kc + code_row(to, q, g) + c0, from.kc + code_row(from, p, g) + c0, n * cb);
-    copy_bytes(to.vc + code_row(to, q, g) + c0, from.vc + code_row(from, p, g) + c0, n * cb);
-    copy_bytes(to.ks + scale_row(to, q, g) + s0, from.ks + scale_row(from, p, g) + s0, n * sb);
-    copy_bytes(to.vs + scale_row(to, q, g) + s0, from.vs + scale_row(from, p, g) + s0, n * sb);
+    constexpr int kAhead = 5;
+    const int n = t1 - t0, cb = n * (from.d / 2) / 16, sb = n * (from.d / kGroup) / 16;  // whole pieces
+    const size_t cf = code_row(from, p, g) + (size_t)t0 * (from.d / 2), ct = code_row(to, q, g) + (size_t)t0 * (from.d / 2);
+    const size_t sf = scale_row(from, p, g) + (size_t)t0 * (from.d / kGroup);
+    const size_t st = scale_row(to, q, g) + (size_t)t0 * (from.d / kGroup);
+    const uint4* src[4] = {reinterpret_cast<const uint4*>(from.kc + cf), reinterpret_cast<const uint4*>(from.vc + cf),
+                           reinterpret_cast<const uint4*>(from.ks + sf), reinterpret_cast<const uint4*>(from.vs + sf)};
+    uint4* dst[4] = {reinterpret_cast<uint4*>(to.kc + ct), reinterpret_cast<uint4*>(to.vc + ct),
+                     reinterpret_cast<uint4*>(to.ks + st), reinterpret_cast<uint4*>(to.vs + st)};
+    const int all = 2 * (cb + sb);
+    auto where = [&](int i, int& which) {  // the i-th piece
+        which = i < cb ? 0 : i < 2 * cb ? 1 : i < 2 * cb + sb ? 2 : 3;
+        return which == 0 ? i : which == 1 ? i - cb : which == 2 ? i - 2 * cb : i - 2 * cb - sb;
+    };
+    for (int i0 = threadIdx.x; i0 < all; i0 += kThreads * kAhead) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * kThreads;
+            int which;
+            const int at = where(i, which);
+            if (i < all) x[j] = __ldcs((which == 0 ? src[0] : which == 1 ? src[1] : which == 2 ? src[2] : src[3]) + at);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * kThreads;
+            int which;
+            const int at = where(i, which);
+            if (i < all) (which == 0 ? dst[0] : which == 1 ? dst[1] : which == 2 ? dst[2] : dst[3])[at] = x[j];
+        }
+    }
+    const int words = n * (from.d / kGroup) / 4 - 4 * sb;  // of each kind of scales
+    if (threadIdx.x < 2 * words) {
+        const bool v = threadIdx.x >= words;
+        const int at = 4 * sb + threadIdx.x - (v ? words : 0);
+        reinterpret_cast<uint32_t*>(v ? dst[3] : dst[2])[at] = reinterpret_cast<const uint32_t*>(v ? src[3] : src[2])[at];
+    }
 }
 
 // CTA (pair, head, slice): the slice's tokens of the pair's partial page; slice 0 of head 0 also
 // writes the row, the references and the length.
 __global__ void __launch_bounds__(kThreads)
 fork_kernel(View c, const int* __restrict__ src, const int* __restrict__ dst, int n, const int* __restrict__ ws) {
-    if (!ws[kVerdict]) return;
+    cudaGridDependencySynchronize();
+    if (!__ldcg(ws + kVerdict)) return;
     const int *len = ws + kLists, *copy = len + n, *list = copy + n;
     const int i = blockIdx.x, g = blockIdx.y, z = blockIdx.z;
     const int L = len[i], full = L / c.chunk, rest = L % c.chunk;
@@ -247,6 +273,7 @@ __global__ void __launch_bounds__(kThreads) free_kernel(View c, const int* __res
 
 // ws lists: the page's new number or -1 [pages].
 __global__ void __launch_bounds__(kPlan) compact_plan_kernel(View c, View to, int* ws) {
+    cudaTriggerProgrammaticLaunchCompletion();
     int* name = ws + kLists;
     int live = 0;
     for (int p0 = 0; p0 < c.pages; p0 += kPlan) {
@@ -266,7 +293,8 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(View c, View to, in
 
 // CTA (page, head, slice) copies; CTAs behind the pages write the tables.
 __global__ void __launch_bounds__(kThreads) compact_kernel(View c, View to, const int* __restrict__ ws) {
-    if (!ws[kVerdict]) return;
+    cudaGridDependencySynchronize();
+    if (!__ldcg(ws + kVerdict)) return;
     const int* name = ws + kLists;
     const int p = blockIdx.x, g = blockIdx.y, z = blockIdx.z;
     if (p < c.pages) {
@@ -274,8 +302,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(View c, View to, cons
         if (q < 0) return;
         if (z == 0) {
             if (g == 0 && threadIdx.x == 0) to.refs[q] = c.refs[p];
-            copy_bytes(reinterpret_cast<uint8_t*>(to.mean + ((size_t)q * c.hkv + g) * c.d),
-                       reinterpret_cast<const uint8_t*>(c.mean + ((size_t)p * c.hkv + g) * c.d), 4 * c.d);
+            for (int i = threadIdx.x; i < c.d; i += kThreads)
+                to.mean[((size_t)q * c.hkv + g) * c.d + i] = c.mean[((size_t)p * c.hkv + g) * c.d + i];
         }
         const int t0 = z * kCopyTokens;
         copy_tokens(to, q, c, p, g, t0, min(c.chunk, t0 + kCopyTokens));
@@ -308,8 +336,7 @@ cudaError_t launch_fork(const View& c, const int* src, const int* dst, int n, in
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int slices = (c.chunk + kCopyTokens - 1) / kCopyTokens;
-    fork_kernel<<<dim3(n, c.hkv, slices), kThreads, 0, st>>>(c, src, dst, n, ws);
-    return cudaGetLastError();
+    return launch_early(fork_kernel, dim3(n, c.hkv, slices), kThreads, 0, st, c, src, dst, n, (const int*)ws);
 }
 
 cudaError_t launch_free(const View& c, const int* seqs, int n, cudaStream_t st) {
@@ -323,8 +350,7 @@ cudaError_t launch_compact(const View& c, const View& into, int* ws, cudaStream_
     if (e != cudaSuccess) return e;
     const int slices = (c.chunk + kCopyTokens - 1) / kCopyTokens;
     const int tables = 16;
-    compact_kernel<<<dim3(c.pages + tables, c.hkv, slices), kThreads, 0, st>>>(c, into, ws);
-    return cudaGetLastError();
+    return launch_early(compact_kernel, dim3(c.pages + tables, c.hkv, slices), kThreads, 0, st, c, into, (const int*)ws);
 }
 
 }  // namespace cache
