@@ -14,7 +14,6 @@
 #include <cooperative_groups.h>
 
 #include "cache_internal.cuh"
-#include "moba_internal.cuh"
 #include "ptx.cuh"
 
 namespace moba {
@@ -44,35 +43,43 @@ __device__ __forceinline__ Row row_of(const View& c, const DecodeArgs& a, int r)
     return w;
 }
 
-// Tokens of a sequence, 0 where the length is out of range.
-__device__ __forceinline__ int held_tokens(const View& c, int seq) {
-    const int L = __ldg(c.lengths + seq);
-    return L < 0 || L > (long long)c.max_blocks * c.chunk ? 0 : L;
+// A score as an integer of the same order (-0 as +0); a NaN ranks with -inf, behind the others.
+__device__ __forceinline__ int order_of(float x) {
+    const int b = __float_as_int((x == x ? x : -INFINITY) + 0.f);
+    return b ^ (b >> 31 & 0x7fffffff);
 }
 
-// Inserts a warp's candidates (lane by lane) into its sorted lists' best n, by n rounds of a warp
-// argmax over the lists' heads in the order (score descending, block ascending): out(i, score, block).
-template <int K, typename F>
-__device__ __forceinline__ void take_best(float (&val)[K], int (&idx)[K], int n, F out) {
-    for (int i = 0; i < n; ++i) {
-        float bv = val[0];
-        int bi = idx[0];
+// Inserts (x, id) into a list sorted by (score descending, block ascending).
+template <int K>
+__device__ __forceinline__ void insert_key(int (&val)[K], int (&idx)[K], int x, int id) {
+    bool gt[K];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            const float ov = __shfl_xor_sync(0xffffffffu, bv, off);
-            const int oi = __shfl_xor_sync(0xffffffffu, bi, off);
-            if (ov > bv || (ov == bv && oi < bi)) {
-                bv = ov;
-                bi = oi;
-            }
+    for (int i = 0; i < K; ++i) gt[i] = x > val[i] || (x == val[i] && id < idx[i]);
+    if (gt[K - 1]) {
+#pragma unroll
+        for (int i = K - 1; i > 0; --i) {
+            val[i] = gt[i] ? (gt[i - 1] ? val[i - 1] : x) : val[i];
+            idx[i] = gt[i] ? (gt[i - 1] ? idx[i - 1] : id) : idx[i];
         }
-        if (idx[0] == bi) {
+        val[0] = gt[0] ? x : val[0];
+        idx[0] = gt[0] ? id : idx[0];
+    }
+}
+
+// The best n of the lanes' lists: n rounds of two warp reductions over the lists' heads (the largest
+// score, then its lowest block), out(i, score, block).
+template <int K, typename F>
+__device__ __forceinline__ void take_best(int (&val)[K], int (&idx)[K], int n, F out) {
+    for (int i = 0; i < n; ++i) {
+        const int bv = __reduce_max_sync(0xffffffffu, val[0]);
+        const int bi = __reduce_min_sync(0xffffffffu, val[0] == bv ? idx[0] : INT_MAX);
+        if (val[0] == bv && idx[0] == bi) {
 #pragma unroll
             for (int k = 0; k + 1 < K; ++k) {
                 val[k] = val[k + 1];
                 idx[k] = idx[k + 1];
             }
-            val[K - 1] = -INFINITY;
+            val[K - 1] = INT_MIN;
             idx[K - 1] = INT_MAX;
         }
         out(i, bv, bi);
@@ -90,23 +97,34 @@ constexpr int kBatch = 2;
 template <int D, int K>
 __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs a, DecodeWs ws) {
     constexpr int V = D / 32;  // float4s of a lane
+    constexpr int kMasks = kRowHeads * kWindow * 4;  // blocks whose heads fit the scores' memory
     __shared__ float4 qs[kRowHeads][D / 4];
-    __shared__ float score[kRowHeads][kWindow];
-    __shared__ float best_v[kRowHeads * 32];
-    __shared__ int best_i[kRowHeads * 32];
-    __shared__ int pick[kRowHeads * 32];
+    __shared__ int score[kRowHeads][kWindow];
+    __shared__ int best_v[kRowHeads * 32], best_i[kRowHeads * 32], pick[kRowHeads * 32];
+    __shared__ int warp_sum[kThreads / 32];
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     const int cs = cluster.num_blocks(), rank = cluster.block_rank();
     cudaTriggerProgrammaticLaunchCompletion();
     const int r = blockIdx.x / cs, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Row w = row_of(c, a, r);
-    const int L = held_tokens(c, w.seq);
+    const int* row = c.table + (size_t)w.seq * c.max_blocks;
+    // loads that do not wait for one another: the length, the queries (8 bytes a thread), the first pages
+    const int raw_len = __ldg(c.lengths + w.seq);
+    const uint2 q4 = tid < w.nh * (D / 4)
+                         ? __ldg(reinterpret_cast<const uint2*>(a.q + ((size_t)w.seq * a.hq + w.h0) * D) + tid)
+                         : make_uint2(0, 0);
+    const int lane_block = (warp * 4 + (lane >> 3)) * kBatch;
+    int page[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+        page[u] = a.topk > 1 && cs == 1 && lane_block + u < c.max_blocks ? __ldg(row + lane_block + u) : -1;
+    const int L = raw_len < 0 || raw_len > (long long)c.max_blocks * c.chunk ? 0 : raw_len;
     if (L == 0) {
         if (rank) return;
         if (tid == 0) {
             ws.tiles[r] = 0;
-            if (__ldg(c.lengths + w.seq) != 0) report(c, MOBA_ERR_INVALID_ARG);
+            if (raw_len != 0) report(c, MOBA_ERR_INVALID_ARG);
         }
         for (int i = tid; i < w.nh * D; i += kThreads)
             a.out[((size_t)w.seq * a.hq + w.h0) * D + i] = __float2bfloat16(0.f);
@@ -114,7 +132,6 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs
         return;
     }
     const int own = (L - 1) / c.chunk;
-    const int* row = c.table + (size_t)w.seq * c.max_blocks;
     int2* items = ws.items + (size_t)r * a.max_items;
     const int all = (1 << w.nh) - 1;
     const int own_tiles = (L - own * c.chunk + kTile - 1) / kTile, per_block = c.chunk / kTile;
@@ -128,15 +145,13 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs
             for (int j = first + tid; j <= own; j += kThreads) items[j - first] = make_int2(__ldg(row + j), all);
         return;
     }
-    for (int i = tid; i < kRowHeads * D; i += kThreads) {
-        const int h = i / D;
-        reinterpret_cast<float*>(qs)[i] = h < w.nh ? __bfloat162float(a.q[((size_t)w.seq * a.hq + w.h0) * D + i]) : 0.f;
-    }
-    float val[K];
-    int idx[K];
+    reinterpret_cast<float4*>(qs)[tid] =  // D / 4 * kRowHeads <= kThreads
+        make_float4(__uint_as_float(q4.x << 16), __uint_as_float(q4.x & 0xffff0000u), __uint_as_float(q4.y << 16),
+                    __uint_as_float(q4.y & 0xffff0000u));
+    int val[K], idx[K];
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-        val[i] = -INFINITY;
+        val[i] = INT_MIN;
         idx[i] = INT_MAX;
     }
     const int l8 = lane & 7;
@@ -144,15 +159,14 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs
     for (int start = rank * span; start < own; start += cs * span) {
         const int n = min(span, own - start);
         __syncthreads();
-        for (int b = (warp * 4 + (lane >> 3)) * kBatch; b < (n + 4 * kBatch - 1) / (4 * kBatch) * (4 * kBatch);
-             b += kThreads / 32 * 4 * kBatch) {
+        for (int b = lane_block; b < (n + 4 * kBatch - 1) / (4 * kBatch) * (4 * kBatch); b += kThreads / 32 * 4 * kBatch) {
             float4 x[kBatch][V];
             bool ok[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                const int page = b + u < n ? __ldg(row + start + b + u) : -1;
-                ok[u] = (unsigned)page < (unsigned)c.pages;
-                const float4* m = reinterpret_cast<const float4*>(c.mean + ((size_t)(ok[u] ? page : 0) * c.hkv + w.g) * D);
+                const int p = b + u >= n ? -1 : cs == 1 && start + b == lane_block ? page[u] : __ldg(row + start + b + u);
+                ok[u] = (unsigned)p < (unsigned)c.pages;
+                const float4* m = reinterpret_cast<const float4*>(c.mean + ((size_t)(ok[u] ? p : 0) * c.hkv + w.g) * D);
 #pragma unroll
                 for (int i = 0; i < V; ++i) x[u][i] = ok[u] ? __ldg(m + l8 + 8 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
@@ -164,32 +178,32 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs
                     for (int u = 0; u < kBatch; ++u) s[u] = 0.f;
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        const float4 q4 = qs[h][l8 + 8 * i];
+                        const float4 y = qs[h][l8 + 8 * i];
 #pragma unroll
                         for (int u = 0; u < kBatch; ++u) {
-                            s[u] = fmaf(q4.x, x[u][i].x, s[u]);
-                            s[u] = fmaf(q4.y, x[u][i].y, s[u]);
-                            s[u] = fmaf(q4.z, x[u][i].z, s[u]);
-                            s[u] = fmaf(q4.w, x[u][i].w, s[u]);
+                            s[u] = fmaf(y.x, x[u][i].x, s[u]);
+                            s[u] = fmaf(y.y, x[u][i].y, s[u]);
+                            s[u] = fmaf(y.z, x[u][i].z, s[u]);
+                            s[u] = fmaf(y.w, x[u][i].w, s[u]);
                         }
                     }
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u) {
 #pragma unroll
                         for (int off = 4; off > 0; off >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], off);
-                        // a NaN, and a page that is not there, ranks last
-                        if (l8 == h && b + u < n) score[h][b + u] = ok[u] && s[u] == s[u] ? s[u] : -INFINITY;
+                        // a page that is not there ranks with the NaNs
+                        if (l8 == h && b + u < n) score[h][b + u] = order_of(ok[u] ? s[u] : -INFINITY);
                     }
                 }
             }
         }
         __syncthreads();
         if (warp < w.nh)
-            for (int j = lane; j < n; j += 32) insert_ordered<K>(val, idx, score[warp][j], start + j);
+            for (int j = lane; j < n; j += 32) insert_key<K>(val, idx, score[warp][j], start + j);
     }
     // warp = head
     if (warp < w.nh)
-        take_best<K>(val, idx, n_route, [&](int i, float v, int j) {
+        take_best<K>(val, idx, n_route, [&](int i, int v, int j) {
             if (lane == 0) {
                 best_v[warp * n_route + i] = v;
                 best_i[warp * n_route + i] = j;
@@ -201,47 +215,61 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs
         if (rank == 0 && warp < w.nh) {
 #pragma unroll
             for (int i = 0; i < K; ++i) {
-                val[i] = -INFINITY;
+                val[i] = INT_MIN;
                 idx[i] = INT_MAX;
             }
             for (int i = lane; i < cs * n_route; i += 32) {
                 const int from = i / n_route, at = warp * n_route + i - from * n_route;
-                insert_ordered<K>(val, idx, cluster.map_shared_rank(best_v, from)[at],
-                                  cluster.map_shared_rank(best_i, from)[at]);
+                insert_key<K>(val, idx, cluster.map_shared_rank(best_v, from)[at],
+                              cluster.map_shared_rank(best_i, from)[at]);
             }
-            take_best<K>(val, idx, n_route, [&](int i, float, int j) {
+            take_best<K>(val, idx, n_route, [&](int i, int, int j) {
                 if (lane == 0) pick[warp * n_route + i] = j;
             });
         }
         cluster.sync();  // the lists have been read
         if (rank) return;
     }
-    __syncthreads();
-    // union of the heads' choices: a block's first mention leads; it counts the leaders before it
+    // Union of the heads' choices, ascending: the blocks' head masks, a byte each, in the scores'
+    // memory (kMasks blocks at a time; a list this long is cut into pieces), then a scan over them.
+    unsigned* masks = reinterpret_cast<unsigned*>(score);
     const int n = w.nh * n_route;
-    __shared__ int lead[kRowHeads * 32];
-    int mine = -1, mask = 0;
-    if (tid < n) {
-        mine = pick[tid];
-        bool first = true;
-        for (int i = 0; i < n; ++i)
-            if (pick[i] == mine) {
-                mask |= 1 << (i / n_route);
-                first = first && i >= tid;
+    int listed = 0;
+    for (int base = 0; base < own; base += kMasks) {
+        const int words = (min(kMasks, own - base) + 3) / 4, per = (words + kThreads - 1) / kThreads;
+        __syncthreads();
+        for (int i = tid; i < words; i += kThreads) masks[i] = 0;
+        __syncthreads();
+        if (tid < n) {
+            const int j = pick[tid] - base;
+            if (j >= 0 && j < kMasks) atomicOr(masks + (j >> 2), 1u << (tid / n_route) << 8 * (j & 3));
+        }
+        __syncthreads();
+        int mine = 0;
+        for (int i = tid * per; i < min(words, (tid + 1) * per); ++i)
+            for (int k = 0; k < 4; ++k) mine += (masks[i] >> 8 * k & 0xff) != 0;
+        int upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
+        }
+        if (lane == 31) warp_sum[warp] = upto;
+        __syncthreads();
+        int at = listed + upto - mine;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) at += warp_sum[i];
+            listed += warp_sum[i];
+        }
+        for (int i = tid * per; i < min(words, (tid + 1) * per) && mine; ++i)
+            for (int k = 0; k < 4; ++k) {
+                const int heads = masks[i] >> 8 * k & 0xff;
+                if (heads) items[at++] = make_int2(__ldg(row + base + 4 * i + k), heads);
             }
-        lead[tid] = first;
-        if (!first) mine = -1;
     }
-    __syncthreads();
-    if (mine >= 0) {
-        int at = 0;
-        for (int i = 0; i < n; ++i) at += lead[i] && pick[i] < mine;
-        items[at] = make_int2(__ldg(row + mine), mask);
-    }
-    const int leaders = __syncthreads_count(mine >= 0);
     if (tid == 0) {
-        items[leaders] = make_int2(__ldg(row + own), all);
-        ws.tiles[r] = leaders * per_block + own_tiles;
+        items[listed] = make_int2(__ldg(row + own), all);
+        ws.tiles[r] = listed * per_block + own_tiles;
     }
 }
 
