@@ -6,9 +6,10 @@
 // nearest with ties to even; the held value is c s.  Six is the largest e2m1 magnitude, so the
 // group's maximum lands on the last step of the grid.  Streaming: 4 bytes are read per key and
 // value channel pair and 1.125 written.
-//   append_kernel        one CTA per (64-position segment of a sequence's new tokens, some KV heads)
-//   append_means_kernel  one CTA per (completed block, KV head), and one warp per sequence that
-//                        moves its length
+//   append_blocks_kernel   one CTA per (block that gets new tokens, KV head): writes them, and the
+//                          mean if they complete the block; one warp per sequence moves its length
+//   append_kernel, append_means_kernel   the same where blocks are long and too few to fill the
+//                          GPU: CTAs of 64 positions, then the means from the pages
 #include "cache_internal.cuh"
 
 namespace moba {
@@ -120,6 +121,145 @@ __device__ __forceinline__ void held_f16(uint2 codes, uint32_t scale, uint32_t (
     }
 }
 
+// One warp: the length of sequence i, where all of its new tokens could be written.  CTAs of the same
+// launch read the length to check that i's first position does not pass it; it never falls below
+// that position here, so they see the same answer before and after.
+__device__ __forceinline__ void move_length(const View& c, const AppendArgs& a, int i) {
+    if (i >= c.seqs) return;
+    const int lane = threadIdx.x & 31;
+    bool bad;
+    const NewTokens t = new_tokens(c, a.cu, a.start, a.total, i, &bad);
+    if (bad && lane == 0) report(c, MOBA_ERR_INVALID_ARG);
+    if (t.n == 0) return;
+    bool ok = true;
+    for (int j = t.first / c.chunk + lane; j <= (t.first + t.n - 1) / c.chunk; j += 32)
+        ok = ok && own_page(c, __ldg(c.table + (size_t)i * c.max_blocks + j));
+    ok = __all_sync(0xffffffffu, ok);
+    if (lane == 0) {
+        if (ok) c.lengths[i] = t.first + t.n;
+        else report(c, MOBA_ERR_INVALID_ARG);
+    }
+}
+
+// Quantises the 16 channels of kind kV at src and writes them to row `at` of a page's head, and the
+// held values where they are wanted.
+template <int D, bool kV>
+__device__ __forceinline__ Quantised put(const View& c, const AppendArgs& a, size_t src, uint8_t* codes,
+                                         uint8_t* scales, size_t at, int grp) {
+    const uint4* x = reinterpret_cast<const uint4*>((kV ? a.v : a.k) + src);
+    const uint4 x0 = __ldcs(x), x1 = __ldcs(x + 1);
+    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    const float unit = kV ? c.v_unit : c.k_unit;
+    const Quantised r = quantise(w, 1.f / unit);  // a power of two
+    *reinterpret_cast<uint2*>(codes + at * (D / 2) + grp * 8) = r.codes;
+    scales[at * (D / kGroup) + grp] = (uint8_t)r.scale;
+    if (a.k_held) {
+        uint32_t h[8], o[8];
+        held_f16(r.codes, r.scale, h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 f = f16x2_to_f32(h[j]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * unit, f.y * unit);
+            o[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        uint4* dst = reinterpret_cast<uint4*>((kV ? a.v_held : a.k_held) + src);
+        __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
+        __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+    }
+    return r;
+}
+
+__device__ __forceinline__ void add_held(float (&acc)[kGroup], uint2 codes, uint32_t scale) {
+    uint32_t h[8];
+    held_f16(codes, scale, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = f16x2_to_f32(h[i]);
+        acc[2 * i] += f.x;
+        acc[2 * i + 1] += f.y;
+    }
+}
+
+// Mean of a page's held keys.  256 threads take (row, group) pairs; each adds the block's rows row,
+// row + kRows, ... in ascending order in fp32, and the rows' sums are added in a fixed order, so
+// the mean is the same bits however the block was filled.  The rows below `upto` are read from the
+// page, eight ahead of the sums.
+template <int D>
+__device__ __forceinline__ void add_rows(float (&acc)[kGroup], const uint8_t* codes, const uint8_t* scales, int upto) {
+    constexpr int kPerTok = D / kGroup, kRows = kThreads / kPerTok, kAhead = 8;
+    const int row = threadIdx.x / kPerTok, grp = threadIdx.x - row * kPerTok;
+    for (int r = row; r < upto; r += kRows * kAhead) {
+        uint2 w[kAhead];
+        uint32_t sc[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int at = r + j * kRows;
+            w[j] = at < upto ? *reinterpret_cast<const uint2*>(codes + (size_t)at * (D / 2) + grp * 8) : make_uint2(0, 0);
+            sc[j] = at < upto ? scales[(size_t)at * kPerTok + grp] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) add_held(acc, w[j], sc[j]);  // those at or behind upto add zeros
+    }
+}
+template <int D>
+__device__ __forceinline__ void write_mean(const float (&acc)[kGroup], const View& c, int page, int g) {
+    constexpr int kPerTok = D / kGroup, kRows = kThreads / kPerTok;
+    __shared__ float sums[kRows][D];
+    const int row = threadIdx.x / kPerTok, grp = threadIdx.x - row * kPerTok;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) sums[row][grp * kGroup + i] = acc[i];
+    __syncthreads();
+    if (threadIdx.x < D) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int r = 0; r < kRows; ++r) s += sums[r][threadIdx.x];
+        c.mean[((size_t)page * c.hkv + g) * D + threadIdx.x] = s * c.k_unit / (float)c.chunk;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+append_blocks_kernel(View c, AppendArgs a, int units) {
+    constexpr int kPerTok = D / kGroup, kRows = kThreads / kPerTok;
+    __shared__ int s_page, s_off, s_end, s_row;
+    const int g = blockIdx.y;
+    if (blockIdx.x >= units) {
+        if (g == 0) move_length(c, a, (blockIdx.x - units) * (kThreads / 32) + (threadIdx.x >> 5));
+        return;
+    }
+    if (threadIdx.x < 32) {
+        NewTokens t;
+        int u;
+        const int seq = find_unit(c, a, c.chunk, false, blockIdx.x, t, u);
+        if (threadIdx.x == 0) {
+            const int page = seq >= 0 ? __ldg(c.table + (size_t)seq * c.max_blocks + u) : -1;
+            s_page = own_page(c, page) ? page : -1;  // else the sequence's mover reports it
+            const int p0 = max(t.first, u * c.chunk), p1 = min(t.first + t.n, (u + 1) * c.chunk);
+            s_off = p0 - u * c.chunk;
+            s_end = p1 - u * c.chunk;
+            s_row = t.row + p0 - t.first;
+        }
+    }
+    __syncthreads();
+    if (s_page < 0) return;
+    const int off = s_off, end = s_end, page = s_page;
+    const int row = threadIdx.x / kPerTok, grp = threadIdx.x - row * kPerTok;
+    const size_t crow = code_row(c, page, g), srow = scale_row(c, page, g);
+    const int first = off + (row - off % kRows + kRows) % kRows;  // this thread's first new row
+    const size_t src = ((size_t)(s_row - off) * c.hkv + g) * D + grp * kGroup, step = (size_t)c.hkv * D;
+    float acc[kGroup];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) acc[i] = 0.f;
+    const bool complete = end == c.chunk;
+    if (complete && off) add_rows<D>(acc, c.kc + crow, c.ks + srow, off);
+    for (int r = first; r < end; r += kRows) {
+        const Quantised q = put<D, false>(c, a, src + r * step, c.kc + crow, c.ks + srow, r, grp);
+        if (complete) add_held(acc, q.codes, q.scale);
+    }
+    for (int r = first; r < end; r += kRows) put<D, true>(c, a, src + r * step, c.vc + crow, c.vs + srow, r, grp);
+    if (complete) write_mean<D>(acc, c, page, g);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 append_kernel(View c, AppendArgs a, int heads) {
@@ -157,64 +297,30 @@ append_kernel(View c, AppendArgs a, int heads) {
         e -= g * per_head;
         const int tok = e / kPerTok, grp = e - tok * kPerTok;
         const size_t src = ((size_t)(s_row + tok) * c.hkv + g0 + g) * D + grp * kGroup;
-        const uint4* x = reinterpret_cast<const uint4*>((is_v ? a.v : a.k) + src);
-        const uint4 x0 = __ldcs(x), x1 = __ldcs(x + 1);
-        const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-        const float unit = is_v ? c.v_unit : c.k_unit;
-        const Quantised r = quantise(w, 1.f / unit);  // a power of two
         const size_t at = (size_t)g * c.chunk + s_off + tok;
-        *reinterpret_cast<uint2*>((is_v ? c.vc : c.kc) + crow + at * (D / 2) + grp * 8) = r.codes;
-        ((is_v ? c.vs : c.ks) + srow)[at * kPerTok + grp] = (uint8_t)r.scale;
-        if (a.k_held) {
-            uint32_t h[8], o[8];
-            held_f16(r.codes, r.scale, h);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 f = f16x2_to_f32(h[j]);
-                const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * unit, f.y * unit);
-                o[j] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            uint4* dst = reinterpret_cast<uint4*>((is_v ? a.v_held : a.k_held) + src);
-            __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
-            __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
-        }
+        if (is_v)
+            put<D, true>(c, a, src, c.vc + crow, c.vs + srow, at, grp);
+        else
+            put<D, false>(c, a, src, c.kc + crow, c.ks + srow, at, grp);
     }
 }
 
-// Mean of the held keys of each block that the new tokens complete, from the page itself: 256
-// threads take (row, group) pairs, each adds its rows in ascending order in fp32, and the rows'
-// sums are added in a fixed order, so the mean does not depend on how the block was filled.
-// CTAs behind `blocks` move the lengths.
+// The means of the blocks that the new tokens complete; CTAs behind `blocks` move the lengths.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 append_means_kernel(View c, AppendArgs a, int blocks) {
-    constexpr int kPerTok = D / kGroup, kRows = kThreads / kPerTok;
-    __shared__ float sums[kRows][D];
     __shared__ int s_page;
-    const int tid = threadIdx.x, lane = tid & 31, g = blockIdx.y;
+    const int g = blockIdx.y;
     if (blockIdx.x >= blocks) {
         cudaGridDependencySynchronize();  // the kernel before this one reads the lengths
-        const int i = (blockIdx.x - blocks) * (kThreads / 32) + (tid >> 5);
-        if (g || i >= c.seqs) return;
-        bool bad;
-        const NewTokens t = new_tokens(c, a.cu, a.start, a.total, i, &bad);
-        if (bad && lane == 0) report(c, MOBA_ERR_INVALID_ARG);
-        if (t.n == 0) return;
-        bool ok = true;
-        for (int j = t.first / c.chunk + lane; j <= (t.first + t.n - 1) / c.chunk; j += 32)
-            ok = ok && own_page(c, __ldg(c.table + (size_t)i * c.max_blocks + j));
-        ok = __all_sync(0xffffffffu, ok);
-        if (lane == 0) {
-            if (ok) c.lengths[i] = t.first + t.n;
-            else report(c, MOBA_ERR_INVALID_ARG);
-        }
+        if (g == 0) move_length(c, a, (blockIdx.x - blocks) * (kThreads / 32) + (threadIdx.x >> 5));
         return;
     }
-    if (tid < 32) {
+    if (threadIdx.x < 32) {
         NewTokens t;
         int u;
         const int seq = find_unit(c, a, c.chunk, true, blockIdx.x, t, u);
-        if (tid == 0) {
+        if (threadIdx.x == 0) {
             const int page = seq >= 0 ? __ldg(c.table + (size_t)seq * c.max_blocks + u) : -1;
             s_page = own_page(c, page) ? page : -1;
         }
@@ -222,43 +328,11 @@ append_means_kernel(View c, AppendArgs a, int blocks) {
     __syncthreads();
     if (s_page < 0) return;
     cudaGridDependencySynchronize();
-    const uint8_t* codes = c.kc + code_row(c, s_page, g);
-    const uint8_t* scales = c.ks + scale_row(c, s_page, g);
-    const int row = tid / kPerTok, grp = tid - row * kPerTok;
     float acc[kGroup];
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) acc[i] = 0.f;
-    // kAhead rows are read before the first is added; those behind the block add zeros
-    constexpr int kAhead = 8;
-    for (int r = row; r < c.chunk; r += kRows * kAhead) {
-        uint2 w[kAhead];
-        uint32_t sc[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int at = r + j * kRows;
-            w[j] = at < c.chunk ? *reinterpret_cast<const uint2*>(codes + (size_t)at * (D / 2) + grp * 8) : make_uint2(0, 0);
-            sc[j] = at < c.chunk ? scales[(size_t)at * kPerTok + grp] : 0;
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            uint32_t h[8];
-            held_f16(w[j], sc[j], h);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f = f16x2_to_f32(h[i]);
-                acc[2 * i] += f.x;
-                acc[2 * i + 1] += f.y;
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kGroup; ++i) sums[row][grp * kGroup + i] = acc[i];
-    __syncthreads();
-    if (tid < D) {
-        float s = 0.f;
-        for (int r = 0; r < kRows; ++r) s += sums[r][tid];
-        c.mean[((size_t)s_page * c.hkv + g) * D + tid] = s * c.k_unit / (float)c.chunk;
-    }
+    add_rows<D>(acc, c.kc + code_row(c, s_page, g), c.ks + scale_row(c, s_page, g), c.chunk);
+    write_mean<D>(acc, c, s_page, g);
 }
 
 template <int D>
@@ -266,6 +340,14 @@ cudaError_t launch_append_d(const View& c, const AppendArgs& a, cudaStream_t st)
     // A sequence with n > 0 new tokens touches at most (n - 1) / kSeg + 2 segments, and no more
     // segments than tokens; it completes at most n / chunk + 1 blocks, and no more than tokens.
     const long long n = a.total;
+    const int movers = (c.seqs + kThreads / 32 - 1) / (kThreads / 32);
+    // Whole blocks, in one launch, where they make at least four CTAs for each of the 148
+    // multiprocessors, or where no CTA has more than 256 tokens.
+    if (n <= 256 || n * c.hkv / c.chunk >= 592) {
+        const long long units = min(n, n / c.chunk + 2LL * c.seqs);
+        append_blocks_kernel<D><<<dim3((unsigned)(units + movers), c.hkv), kThreads, 0, st>>>(c, a, (int)units);
+        return cudaGetLastError();
+    }
     const long long segs = min(n, n / kSeg + 2LL * c.seqs);
     const long long blocks = min(n, n / c.chunk + c.seqs);
     // A CTA takes as many KV heads as leave about eight CTAs to each of the 148 multiprocessors: its
@@ -274,7 +356,6 @@ cudaError_t launch_append_d(const View& c, const AppendArgs& a, cudaStream_t st)
     append_kernel<D><<<dim3((unsigned)segs, (c.hkv + heads - 1) / heads), kThreads, 0, st>>>(c, a, heads);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int movers = (c.seqs + kThreads / 32 - 1) / (kThreads / 32);
     return launch_early(append_means_kernel<D>, dim3((unsigned)(blocks + movers), c.hkv), kThreads, 0, st, c, a, (int)blocks);
 }
 

@@ -82,7 +82,7 @@ __device__ __forceinline__ NewTokens new_tokens(const View& c, const int* __rest
     const bool range_ok = t.row >= 0 && end >= t.row && end <= total;
     t.n = range_ok ? end - t.row : 0;
     bool wrong = !range_ok;
-    if (t.n > 0 && (t.first < 0 || t.first > __ldg(c.lengths + i) ||
+    if (t.n > 0 && (t.first < 0 || t.first > __ldcg(c.lengths + i) ||
                     (long long)t.first + t.n > (long long)c.max_blocks * c.chunk)) {
         wrong = true;
         t.n = 0;

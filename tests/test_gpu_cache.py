@@ -191,6 +191,39 @@ def test_pieces_write_what_one_call_writes():
             assert torch.equal(x, y)
 
 
+def test_long_prompts_whole_or_in_pieces():
+    """Enough blocks that each gets a CTA of its own, against the same prompts in short pieces: the same bits,
+    means too; blocks that earlier tokens began are completed."""
+    rng = np.random.default_rng(14)
+    heads, d, chunk, lens = 8, 64, 128, [5000, 77, 4700]
+    n = sum(lens)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    k, v = (bf16(rng.standard_normal((n, heads, d))).cuda() for _ in "kv")
+    got = []
+    for cuts in ([1.0], [0.004, 1.0], [0.3, 0.31, 0.6, 1.0]):
+        c = KVCache(80, 3, 40, heads, d, chunk)
+        for t in (c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.k_mean):
+            t.view(torch.uint8).zero_()
+        cache_reserve(c, ints(lens))
+        start = np.zeros(3, int)
+        for f in cuts:
+            upto = (np.array(lens) * f).astype(int)
+            rows = [torch.arange(cu[i] + start[i], cu[i] + upto[i]) for i in range(3)]
+            at = torch.cat(rows).cuda()
+            held = cache_append(c, k[at], v[at], ints(np.concatenate([[0], np.cumsum(upto - start)])), ints(start),
+                                return_held=True)
+            start = upto
+        cache_status(c)
+        got.append([t.view(torch.uint8).clone() for t in (c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.k_mean)] +
+                   [c.lengths.clone()])
+        if cuts == [1.0]:
+            for x, h in zip((k, v), held):
+                np.testing.assert_array_equal(host(h), M.values(*M.quantise(host(x))))
+    for other in got[1:]:
+        for x, y in zip(got[0], other):
+            assert torch.equal(x, y)
+
+
 def test_append_takes_tokens_back_and_refuses_gaps():
     rng = np.random.default_rng(12)
     c, m = pair(12, 2, 4, 1, 64, 128)
