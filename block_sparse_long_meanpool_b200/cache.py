@@ -137,7 +137,7 @@ def _call(c, fn, *args):
 
 def _workspace(c, given, need):
     if given is None:
-        return torch.empty(need, dtype=torch.uint8, device=c.device)
+        return c.k_codes.new_empty(need)  # uint8
     if given.device != c.device or not given.is_contiguous():
         _fail(f"workspace must be a contiguous tensor on {c.device}")
     return given
@@ -185,11 +185,11 @@ def cache_decode(c, q, topk, softmax_scale=None, workspace=None, out=None, lse=N
     _need(q, "q", shape, torch.bfloat16, c.device)
     ws = _workspace(c, workspace, c._size((hq, topk), c._lib.moba_cache_decode_workspace_size, hq, topk))
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=c.device)
+        out = torch.empty_like(q)
     else:
         _need(out, "out", shape, torch.bfloat16, c.device)
     if lse is None:
-        lse = torch.empty((hq, c.num_seqs), dtype=torch.float32, device=c.device)
+        lse = c.k_mean.new_empty((hq, c.num_seqs))  # fp32
     else:
         _need(lse, "lse", (hq, c.num_seqs), torch.float32, c.device)
     _call(c, c._lib.moba_cache_decode, q.data_ptr(), hq, topk, softmax_scale or 0.0, ws.data_ptr(),

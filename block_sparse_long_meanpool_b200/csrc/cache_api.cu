@@ -151,8 +151,9 @@ moba_status decode_layout(const moba_cache* c, int hq, int topk, DecodeLayout* L
     L->tiles = align_up(sizeof(int2) * (size_t)L->rows * L->max_items);
     L->done = L->tiles + align_up(4ull * L->rows);
     L->part_o = L->done + align_up(4ull * L->rows);
-    L->part_ml = L->part_o + align_up(4ull * cache::kMaxParts * L->row_heads * c->head_dim);
-    L->total = L->part_ml + align_up(sizeof(float2) * cache::kMaxParts * L->row_heads);
+    const size_t parts = cache::most_parts(L->rows);
+    L->part_ml = L->part_o + align_up(4 * parts * L->row_heads * c->head_dim);
+    L->total = L->part_ml + align_up(sizeof(float2) * parts * L->row_heads);
     return MOBA_OK;
 }
 

@@ -10,6 +10,8 @@
 //                          mean if they complete the block; one warp per sequence moves its length
 //   append_kernel, append_means_kernel   the same where blocks are long and too few to fill the
 //                          GPU: CTAs of 64 positions, then the means from the pages
+#include <cooperative_groups.h>
+
 #include "cache_internal.cuh"
 
 namespace moba {
@@ -141,14 +143,21 @@ __device__ __forceinline__ void move_length(const View& c, const AppendArgs& a, 
     }
 }
 
-// Quantises the 16 channels of kind kV at src and writes them to row `at` of a page's head, and the
-// held values where they are wanted.
+// The 16 channels of one group, as loaded.
+struct Group {
+    uint4 x0, x1;
+};
+__device__ __forceinline__ Group load_group(const __nv_bfloat16* at) {
+    const uint4* x = reinterpret_cast<const uint4*>(at);
+    return Group{__ldcs(x), __ldcs(x + 1)};
+}
+
+// Quantises a group of kind kV (from src of the new rows) and writes it to row `at` of a page's head,
+// and the held values where they are wanted.
 template <int D, bool kV>
-__device__ __forceinline__ Quantised put(const View& c, const AppendArgs& a, size_t src, uint8_t* codes,
+__device__ __forceinline__ Quantised put(const View& c, const AppendArgs& a, const Group& x, size_t src, uint8_t* codes,
                                          uint8_t* scales, size_t at, int grp) {
-    const uint4* x = reinterpret_cast<const uint4*>((kV ? a.v : a.k) + src);
-    const uint4 x0 = __ldcs(x), x1 = __ldcs(x + 1);
-    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    const uint32_t w[8] = {x.x0.x, x.x0.y, x.x0.z, x.x0.w, x.x1.x, x.x1.y, x.x1.z, x.x1.w};
     const float unit = kV ? c.v_unit : c.k_unit;
     const Quantised r = quantise(w, 1.f / unit);  // a power of two
     *reinterpret_cast<uint2*>(codes + at * (D / 2) + grp * 8) = r.codes;
@@ -180,15 +189,16 @@ __device__ __forceinline__ void add_held(float (&acc)[kGroup], uint2 codes, uint
     }
 }
 
-// Mean of a page's held keys.  256 threads take (row, group) pairs; each adds the block's rows row,
-// row + kRows, ... in ascending order in fp32, and the rows' sums are added in a fixed order, so
-// the mean is the same bits however the block was filled.  The rows below `upto` are read from the
-// page, eight ahead of the sums.
-template <int D>
-__device__ __forceinline__ void add_rows(float (&acc)[kGroup], const uint8_t* codes, const uint8_t* scales, int upto) {
-    constexpr int kPerTok = D / kGroup, kRows = kThreads / kPerTok, kAhead = 8;
+// Sum of a page's held keys over rows [from, upto), read from the page kAhead ahead of the sums: 256
+// threads take (row, group) pairs, each adds its rows in ascending order in fp32, and the rows' sums
+// are added in a fixed order.  A held key is a multiple of its scale's last place, so these sums are
+// rounded only where the scales of a channel differ by more than about 2^10.
+template <int D, int kAhead>
+__device__ __forceinline__ void add_rows(float (&acc)[kGroup], const uint8_t* codes, const uint8_t* scales, int from,
+                                         int upto) {
+    constexpr int kPerTok = D / kGroup, kRows = kThreads / kPerTok;
     const int row = threadIdx.x / kPerTok, grp = threadIdx.x - row * kPerTok;
-    for (int r = row; r < upto; r += kRows * kAhead) {
+    for (int r = from + (row - from % kRows + kRows) % kRows; r < upto; r += kRows * kAhead) {
         uint2 w[kAhead];
         uint32_t sc[kAhead];
 #pragma unroll
@@ -201,8 +211,9 @@ __device__ __forceinline__ void add_rows(float (&acc)[kGroup], const uint8_t* co
         for (int j = 0; j < kAhead; ++j) add_held(acc, w[j], sc[j]);  // those at or behind upto add zeros
     }
 }
+// The threads' sums, per channel: total[D] in shared memory, valid for all threads.
 template <int D>
-__device__ __forceinline__ void write_mean(const float (&acc)[kGroup], const View& c, int page, int g) {
+__device__ __forceinline__ void add_up(const float (&acc)[kGroup], float* total) {
     constexpr int kPerTok = D / kGroup, kRows = kThreads / kPerTok;
     __shared__ float sums[kRows][D];
     const int row = threadIdx.x / kPerTok, grp = threadIdx.x - row * kPerTok;
@@ -213,12 +224,13 @@ __device__ __forceinline__ void write_mean(const float (&acc)[kGroup], const Vie
         float s = 0.f;
 #pragma unroll 8
         for (int r = 0; r < kRows; ++r) s += sums[r][threadIdx.x];
-        c.mean[((size_t)page * c.hkv + g) * D + threadIdx.x] = s * c.k_unit / (float)c.chunk;
+        total[threadIdx.x] = s;
     }
+    __syncthreads();
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 append_blocks_kernel(View c, AppendArgs a, int units) {
     constexpr int kPerTok = D / kGroup, kRows = kThreads / kPerTok;
     __shared__ int s_page, s_off, s_end, s_row;
@@ -251,13 +263,20 @@ append_blocks_kernel(View c, AppendArgs a, int units) {
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) acc[i] = 0.f;
     const bool complete = end == c.chunk;
-    if (complete && off) add_rows<D>(acc, c.kc + crow, c.ks + srow, off);
+    if (complete && off) add_rows<D, 4>(acc, c.kc + crow, c.ks + srow, 0, off);
     for (int r = first; r < end; r += kRows) {
-        const Quantised q = put<D, false>(c, a, src + r * step, c.kc + crow, c.ks + srow, r, grp);
+        const size_t at = src + r * step;
+        const Group k = load_group(a.k + at), v = load_group(a.v + at);
+        const Quantised q = put<D, false>(c, a, k, at, c.kc + crow, c.ks + srow, r, grp);
         if (complete) add_held(acc, q.codes, q.scale);
+        put<D, true>(c, a, v, at, c.vc + crow, c.vs + srow, r, grp);
     }
-    for (int r = first; r < end; r += kRows) put<D, true>(c, a, src + r * step, c.vc + crow, c.vs + srow, r, grp);
-    if (complete) write_mean<D>(acc, c, page, g);
+    if (complete) {
+        __shared__ float total[D];
+        add_up<D>(acc, total);
+        if (threadIdx.x < D)
+            c.mean[((size_t)page * c.hkv + g) * D + threadIdx.x] = total[threadIdx.x] * c.k_unit / (float)c.chunk;
+    }
 }
 
 template <int D>
@@ -265,7 +284,6 @@ __global__ void __launch_bounds__(kThreads)
 append_kernel(View c, AppendArgs a, int heads) {
     constexpr int kPerTok = D / kGroup;  // groups of a token
     __shared__ int s_page, s_off, s_cnt, s_row;
-    cudaTriggerProgrammaticLaunchCompletion();
     const int g0 = blockIdx.y * heads, ng = min(heads, c.hkv - g0);
     if (threadIdx.x < 32) {
         NewTokens t;
@@ -299,40 +317,50 @@ append_kernel(View c, AppendArgs a, int heads) {
         const size_t src = ((size_t)(s_row + tok) * c.hkv + g0 + g) * D + grp * kGroup;
         const size_t at = (size_t)g * c.chunk + s_off + tok;
         if (is_v)
-            put<D, true>(c, a, src, c.vc + crow, c.vs + srow, at, grp);
+            put<D, true>(c, a, load_group(a.v + src), src, c.vc + crow, c.vs + srow, at, grp);
         else
-            put<D, false>(c, a, src, c.kc + crow, c.ks + srow, at, grp);
+            put<D, false>(c, a, load_group(a.k + src), src, c.kc + crow, c.ks + srow, at, grp);
     }
 }
 
-// The means of the blocks that the new tokens complete; CTAs behind `blocks` move the lengths.
+// The means of the blocks that the new tokens complete, a cluster of CTAs to each; those behind
+// `blocks` move the lengths.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 append_means_kernel(View c, AppendArgs a, int blocks) {
     __shared__ int s_page;
-    const int g = blockIdx.y;
-    if (blockIdx.x >= blocks) {
-        cudaGridDependencySynchronize();  // the kernel before this one reads the lengths
-        if (g == 0) move_length(c, a, (blockIdx.x - blocks) * (kThreads / 32) + (threadIdx.x >> 5));
+    __shared__ float total[D];
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int cs = cluster.num_blocks(), rank = cluster.block_rank(), unit = blockIdx.x / cs, g = blockIdx.y;
+    if (unit >= blocks) {
+        if (g == 0 && rank == 0) move_length(c, a, (unit - blocks) * (kThreads / 32) + (threadIdx.x >> 5));
         return;
     }
     if (threadIdx.x < 32) {
         NewTokens t;
         int u;
-        const int seq = find_unit(c, a, c.chunk, true, blockIdx.x, t, u);
+        const int seq = find_unit(c, a, c.chunk, true, unit, t, u);
         if (threadIdx.x == 0) {
             const int page = seq >= 0 ? __ldg(c.table + (size_t)seq * c.max_blocks + u) : -1;
             s_page = own_page(c, page) ? page : -1;
         }
     }
     __syncthreads();
-    if (s_page < 0) return;
-    cudaGridDependencySynchronize();
+    const int page = s_page;  // the same in the whole cluster
+    if (page < 0) return;
     float acc[kGroup];
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) acc[i] = 0.f;
-    add_rows<D>(acc, c.kc + code_row(c, s_page, g), c.ks + scale_row(c, s_page, g), c.chunk);
-    write_mean<D>(acc, c, s_page, g);
+    const int part = c.chunk / cs;  // cs divides 128
+    add_rows<D, 8>(acc, c.kc + code_row(c, page, g), c.ks + scale_row(c, page, g), rank * part, (rank + 1) * part);
+    add_up<D>(acc, total);
+    if (cs > 1) cluster.sync();
+    if (rank == 0 && threadIdx.x < D) {
+        float s = total[threadIdx.x];
+        for (int k = 1; k < cs; ++k) s += cluster.map_shared_rank(total, k)[threadIdx.x];
+        c.mean[((size_t)page * c.hkv + g) * D + threadIdx.x] = s * c.k_unit / (float)c.chunk;
+    }
+    if (cs > 1) cluster.sync();  // the sums have been read
 }
 
 template <int D>
@@ -342,8 +370,10 @@ cudaError_t launch_append_d(const View& c, const AppendArgs& a, cudaStream_t st)
     const long long n = a.total;
     const int movers = (c.seqs + kThreads / 32 - 1) / (kThreads / 32);
     // Whole blocks, in one launch, where they make at least four CTAs for each of the 148
-    // multiprocessors, or where no CTA has more than 256 tokens.
-    if (n <= 256 || n * c.hkv / c.chunk >= 592) {
+    // multiprocessors, or where no CTA has more than 256 tokens, so that its loop is short: 16 x 3K
+    // tokens in 256-token blocks (541 CTAs) take 14.5 us this way and 21.1 in segments, 4 x 4K in
+    // 1024-token blocks (160 CTAs) 45 us this way and 30 in segments.
+    if (n <= 256 || c.chunk <= 256 || n * c.hkv / c.chunk >= 592) {
         const long long units = min(n, n / c.chunk + 2LL * c.seqs);
         append_blocks_kernel<D><<<dim3((unsigned)(units + movers), c.hkv), kThreads, 0, st>>>(c, a, (int)units);
         return cudaGetLastError();
@@ -356,7 +386,20 @@ cudaError_t launch_append_d(const View& c, const AppendArgs& a, cudaStream_t st)
     append_kernel<D><<<dim3((unsigned)segs, (c.hkv + heads - 1) / heads), kThreads, 0, st>>>(c, a, heads);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_early(append_means_kernel<D>, dim3((unsigned)(blocks + movers), c.hkv), kThreads, 0, st, c, a, (int)blocks);
+    // 512 rows of a block to a CTA, or an eighth of it where it is longer
+    int cs = 1;
+    while (cs < 8 && c.chunk / cs > 512) cs *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks + movers) * cs, c.hkv);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cs;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, append_means_kernel<D>, c, a, (int)blocks);
 }
 
 }  // namespace

@@ -959,7 +959,7 @@ cudaError_t launch_decode_d(const View& c, const DecodeArgs& a, const DecodeWs& 
         if (e != cudaSuccess) return e;
         if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
     }
-    return launch_early(cache_attn_kernel<D>, dim3(min(num_sms, kMaxCtas)), kWarps * 32, kSmem, st, c, a, ws);
+    return launch_early(cache_attn_kernel<D>, dim3(max(kMinCtas, min(num_sms, kMaxCtas))), kWarps * 32, kSmem, st, c, a, ws);
 }
 
 }  // namespace

@@ -140,18 +140,20 @@ struct DecodeArgs {
     __nv_bfloat16* out;
     float* lse;
 };
-// CTAs of the attention kernel at most (one per SM), its warps, and the parts of rows that they
-// may leave to be merged: two per team of warps (csrc/cache_decode.cu).
+// The attention kernel has one CTA of kAttnWarps warps per multiprocessor, kMinCtas to kMaxCtas of
+// them; a team is a CTA, or a warp where there are more rows than CTAs, and leaves at most two parts
+// of rows to be merged.
 #ifndef CFG_WARPS
 #define CFG_WARPS 12
 #endif
-constexpr int kMaxCtas = 160, kAttnWarps = CFG_WARPS, kMaxParts = 2 * kMaxCtas * kAttnWarps;
+constexpr int kMinCtas = 128, kMaxCtas = 160, kAttnWarps = CFG_WARPS;
+inline size_t most_parts(int rows) { return 2 * (size_t)kMaxCtas * (rows > kMinCtas ? kAttnWarps : 1); }
 struct DecodeWs {
     int2* items;     // [rows, max_items]: (page, heads that attend to it), ascending blocks
     int* tiles;      // [rows]: tiles of each row
     int* done;       // [rows]: teams that have written their part of the row
-    float* part_o;   // [kMaxParts, row heads, d]: unnormalised outputs of a row's part
-    float2* part_ml;  // [kMaxParts, row heads]: its running maximum (log2 units) and sum
+    float* part_o;   // [most_parts, row heads, d]: unnormalised outputs of a row's part
+    float2* part_ml;  // [most_parts, row heads]: its running maximum (log2 units) and sum
 };
 cudaError_t launch_decode(const View& c, const DecodeArgs& a, const DecodeWs& ws, int num_sms, cudaStream_t st);
 

@@ -316,7 +316,7 @@ moba_status moba_cache_reserve(const moba_cache* c, const int* upto, void* works
  *   quantisation, per 16 channels of x * 2^-exp: scale = e4m3(min(max|x| / 6, 448)), code =
  *   e2m1(x / scale), both to nearest, ties to even, saturating; scale 0 gives codes 0; a NaN in
  *   the group gives scale NaN and codes 0.  k_mean of a completed block is the mean of its held
- *   keys, whatever the calls that wrote them.
+ *   keys (fp32 sums), whichever calls wrote them.
  *   k, v            bf16 [new_tokens, Hkv, d] device
  *   cu_new          int32 [num_seqs + 1] device, start int32 [num_seqs] device
  *   k_held, v_held  bf16 [new_tokens, Hkv, d] device or NULL: receive the values as held (for the
