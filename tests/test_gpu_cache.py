@@ -316,7 +316,8 @@ def test_decode_of_more_rows_than_multiprocessors(d, heads, group, topk, longest
     cache_status(c)
 
 
-@pytest.mark.parametrize("blocks,heads,group,topk", [(130, 1, 2, 4), (140, 2, 8, 32), (1300, 1, 1, 9), (9000, 1, 3, 3)])
+@pytest.mark.parametrize("blocks,heads,group,topk", [(130, 1, 2, 4), (140, 2, 8, 32), (1300, 1, 1, 9), (9000, 1, 3, 3),
+                                                     (33000, 1, 2, 5)])
 def test_gate_over_many_blocks(blocks, heads, group, topk):
     """Rows of more blocks than one CTA scores in two rounds, than one window, and than a cluster's windows: the
     choice is the model's.  The pages hold one token's worth of difference: keys and values are the block's own
@@ -726,6 +727,30 @@ def test_a_captured_step_replays():
             for a, b in zip(got, want[topk][i]):
                 assert torch.equal(a, b), (topk, i)
     for c, *_ in runs.values():
+        cache_status(c)
+
+
+def test_two_streams_at_once():
+    """Decode steps of one cache on two streams at the same time, and of two caches: each as it is alone."""
+    rng = np.random.default_rng(43)
+    caches = []
+    for lengths in ([3000, 129, 0, 2000], [700, 700, 700, 5]):
+        c, m = pair(60, 4, 30, 2, 128, 128)
+        fill(c, m, rng, lengths)
+        caches.append(c)
+    q = bf16(rng.standard_normal((4, 8, 128))).cuda()
+    alone = [cache_decode(c, q, k) for c in caches for k in (0, 3)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in alone]
+    for _ in range(20):
+        got = []
+        for s, (c, k) in zip(streams, [(c, k) for c in caches for k in (0, 3)]):
+            with torch.cuda.stream(s):
+                got.append(cache_decode(c, q, k))
+        torch.cuda.synchronize()
+        for (o, l), (o2, l2) in zip(alone, got):
+            assert torch.equal(o, o2) and torch.equal(l, l2)
+    for c in caches:
         cache_status(c)
 
 
