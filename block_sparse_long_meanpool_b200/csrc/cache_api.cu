@@ -143,6 +143,9 @@ moba_status decode_layout(const moba_cache* c, int hq, int topk, DecodeLayout* L
     const long long rows = (long long)c->num_seqs * c->num_kv_heads * L->hgroups;
     if (rows > (1LL << 24))
         return fail(MOBA_ERR_UNSUPPORTED, "num_seqs * num_q_heads too large (%lld rows of heads)", rows);
+    // the attention counts the tiles of all rows in 32 bits
+    if (rows * (((long long)c->max_blocks * c->chunk_size + 63) / 64) > 0x7fffffffLL)
+        return fail(MOBA_ERR_UNSUPPORTED, "num_seqs * query head groups * max_blocks * chunk_size / 64 exceeds 2^31");
     L->rows = (int)rows;
     L->row_heads = group < cache::kRowHeads ? group : cache::kRowHeads;
     const int most = L->row_heads * (topk - 1) + 1;

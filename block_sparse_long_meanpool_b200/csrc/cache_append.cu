@@ -5,7 +5,8 @@
 // power of two):  a = max|x|,  s = e4m3(min(a / 6, 448)),  c = e2m1(x / s), both rounded to
 // nearest with ties to even; the held value is c s.  Six is the largest e2m1 magnitude, so the
 // group's maximum lands on the last step of the grid.  Streaming: 4 bytes are read per key and
-// value channel pair and 1.125 written.
+// value channel pair and 1.125 written (5.125 with the held values).  8 prompts of 32K tokens, 8 heads
+// of 128 channels, held values returned: 430 us, 5.7 TB/s of 6.5.
 //   append_blocks_kernel   one CTA per (block that gets new tokens, KV head): writes them, and the
 //                          mean if they complete the block; one warp per sequence moves its length
 //   append_kernel, append_means_kernel   the same where blocks are long and too few to fill the

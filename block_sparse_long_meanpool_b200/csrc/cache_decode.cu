@@ -22,11 +22,8 @@ namespace cache {
 namespace {
 
 constexpr int kThreads = 256;
-#ifndef CFG_TILE
-#define CFG_TILE 64
-#endif
-constexpr int kTile = CFG_TILE;
-static_assert(kTile >= 16 && 64 % kTile == 0, "a page (a multiple of 128 tokens) holds at least two whole tiles");
+constexpr int kTile = 64;      // tokens of a tile
+static_assert(64 % kTile == 0, "a page (a multiple of 128 tokens) holds at least two whole tiles");
 constexpr int kWindow = 1024;  // blocks scored at a time
 
 struct Row {
@@ -92,7 +89,8 @@ __device__ __forceinline__ void take_best(int (&val)[K], int (&idx)[K], int n, F
 // The CTAs of a cluster share a row: each scores a part of its blocks and lists its heads' best,
 // and the first one picks from the lists.  Eight lanes take a block (a row of k_mean: D fp32, read
 // in 128-byte pieces), a warp kBatch blocks for each of its four groups of lanes at a time, so that
-// a CTA has 64 rows in flight; what bounds the kernel is their latency, not their bytes.
+// a CTA has 64 rows in flight; what bounds the kernel is their latency, not their bytes: 512 rows of
+// 63 blocks (17 MB) take about 8 us, 8 rows of 255 blocks (1 MB, in clusters) about 9.
 constexpr int kBatch = 2;
 template <int D, int K>
 __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs a, DecodeWs ws) {
@@ -287,19 +285,25 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(View c, DecodeArgs
 //                                              interleaving the nibbles of two rows before the
 //                                              conversion (2 operations per 8 codes)
 // One query per head makes N = 8 columns (heads) of each product; tcgen05 would want 128 rows of M
-// and its operands written to shared memory, and the tensor pipe is not what bounds this kernel.
+// and its operands written to shared memory, and the tensor pipe (a quarter busy) is not what bounds
+// this kernel.
 // q is scaled by a power of two per head so that its largest channel is in [2^14, 2^15): fp16 then
 // holds every channel down to 2^-28 of the largest one exactly, and the rest to 2^-39 of it.
-// p <= 1 is rounded to fp16 (2^-11 relative, an eighth of the bf16 output's own rounding; below
-// 2^-14 an absolute 2^-25, against a sum of at least 1); the sum l is taken before that rounding.
+// p is rounded to fp16 (2^-11 relative, an eighth of the bf16 output's own rounding; below 2^-14 an
+// absolute 2^-25, against a sum of at least 1); the sum l is taken before that rounding.
+//
+// What bounds it: instructions.  A tile of 64 tokens and 128 channels is 9.2 KB and takes a warp
+// about 1100 instructions, half of them on the ALU pipe (256 conversions, the bytes' extraction, the
+// interleaving) and 256 scale products on the FMA pipe, 490 cycles of a multiprocessor, where its share
+// of HBM would allow 390.  32 caches of 16K-32K tokens, 4 query heads to a KV head, every block: 192 us,
+// 4.6 TB/s; the same loop without the arithmetic takes 142 us.  Tried and not kept, same case: 8 warps
+// with rings of two tiles 201 us, 16 warps (spills) 190 us but slower on short rows, tiles of 32 tokens
+// 222 us, half-tile rings 199 us, two accumulators a product and other instruction orders 190-203 us.
 
 constexpr int kWarps = kAttnWarps;
 constexpr int kSmem = 232448;  // shared memory of a CTA
-
-#ifndef CFG_DEPTH
-#define CFG_DEPTH 3
-#endif
-constexpr float kLag = 8.f;
+constexpr int kDepth = 3;      // tiles of a warp's ring at most
+constexpr float kLag = 8.f;    // how far (log2) scores may pass the exponentials' reference
 
 // A tile in shared memory.
 template <int D>
@@ -313,12 +317,12 @@ struct Tile {
 template <int D>
 struct Smem {
     static constexpr int kMisc = 0;  // abort flag, last flag, scan
-    static constexpr int kMl = 8 + 24 * kWarps;   // [warps][heads] float2
+    static constexpr int kMl = 8 + 8 * kWarps + 16;   // [warps][heads] float2
     static constexpr int kState = (kMl + kWarps * kRowHeads * 8 + 127) / 128 * 128;  // [warps][row heads][D] fp32
     __host__ __device__ static int ring(int heads) { return kState + kWarps * heads * D * 4; }
     __host__ __device__ static int depth(int heads) {  // tiles of a warp's ring
         const int n = (kSmem - ring(heads)) / (kWarps * (Tile<D>::kBytes + 16));
-        return n < CFG_DEPTH ? n : CFG_DEPTH;
+        return n < kDepth ? n : kDepth;
     }
 };
 
@@ -363,10 +367,31 @@ struct Segment {
     int row, at, t0, n;  // row; first tile as counted from begin; as counted in the row; tiles
     int row_n;           // tiles of the whole row
 };
+// Exclusive prefix sum over the CTA's threads (sums: kWarps ints of shared memory); total: the sum.
+__device__ __forceinline__ int scan_threads(int x, int* sums, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int upto = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += y;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int before = upto - x;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        const int n = sums[i];
+        if (i < warp) before += n;
+        total += n;
+    }
+    return before;
+}
 __device__ __forceinline__ void next_segment(Segment& s, const int* __restrict__ tiles, int total) {
     s.at += s.n;
     s.t0 = 0;
-    do s.row_n = __ldcg(tiles + ++s.row);
+    do s.row_n = tiles[++s.row];
     while (s.row_n == 0);
     s.n = min(s.row_n, total - s.at);
 }
@@ -382,7 +407,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
     const uint32_t base = ptx::smem_u32(smem);
     volatile int* abort_flag = reinterpret_cast<int*>(smem + S::kMisc);
-    long long* scan = reinterpret_cast<long long*>(smem + S::kMisc + 8);
+    int* scan = reinterpret_cast<int*>(smem + S::kMisc + 8);
     const int depth = S::depth(a.row_heads);  // the warp's ring, its barriers and metas
     const int ring = S::ring(a.row_heads) + warp * depth * T::kBytes;
     const int bars = S::ring(a.row_heads) + kWarps * depth * T::kBytes + warp * depth * 16, metas = bars + 8 * depth;
@@ -396,96 +421,70 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
     // Every CTA adds up the rows' tiles: thread i takes a contiguous part of the rows.
     const int per_thread = (a.rows + kWarps * 32 - 1) / (kWarps * 32);
     const int r0 = min(a.rows, tid * per_thread), r1 = min(a.rows, r0 + per_thread);
-    long long mine = 0;
-    for (int r = r0; r < r1; ++r) mine += __ldcg(ws.tiles + r);
-    long long incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    long long before = incl - mine, all_tiles = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) before += scan[i];
-        all_tiles += scan[i];
-    }
+    int mine = 0;
+    for (int r = r0; r < r1; ++r) mine += ws.tiles[r];
+    int all_tiles;
+    const int before = scan_threads(mine, scan, all_tiles);
+
     // Where there are more rows than CTAs, a team is one warp, and no warp waits for its CTA at a
     // row's end; with fewer rows a row has so many parts that CTAs have to merge their own first.
     const int tn = a.rows > gridDim.x ? 1 : kWarps;
     const int tw = tn == 1 ? 0 : warp, team = tn == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
-    const int me = tn == 1 ? lane : tid;
     Segment seg;
     seg.at = 0;
-    int total;               // the team's tiles
-    long long row_start = 0;  // first tile of seg's row among all tiles
-    long long share = 0, extra = 0;  // tiles of a team: share, one more for the first `extra` teams
+    int total;          // the team's tiles
+    int row_start = 0;  // first tile of seg's row among all tiles
+    int share = 0, extra = 0;  // tiles of a team: share, one more for the first `extra` teams
     int first_team = -1, row_teams = 0;  // where every team keeps to one row: the row's teams
     // A CTA that passes from one row to the next merges and starts twice, which costs about nine
     // tiles' time.  Where that is more than what keeping to one row costs (a row's CTAs are a whole
     // number, so the fullest has up to rows / (CTAs - rows) more tiles than the average), it does.
     const int spare = (int)gridDim.x - a.rows;
-    if (spare > 0 && all_tiles * a.rows < 9LL * gridDim.x * spare) {
-        const int most = max((int)((unsigned)all_tiles + spare - 1) / spare, kWarps);  // tiles of a CTA
-        const int n = r0 < r1 ? ((int)mine + most - 1) / most : 0;  // CTAs of this thread's row (rows < threads)
-        int upto = n;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += y;
+    int* found = scan + 2 * kWarps;  // what the thread that holds a row tells the CTA
+    if (spare > 0 && (long long)all_tiles * a.rows < 9LL * gridDim.x * spare) {
+        const int most = max((all_tiles + spare - 1) / spare, kWarps);  // tiles of a CTA
+        const int n = (mine + most - 1) / most;  // CTAs of this thread's row (there are fewer rows than threads)
+        int ctas;
+        const int from = scan_threads(n, scan + kWarps, ctas);
+        if ((int)blockIdx.x >= ctas) return;
+        if ((int)blockIdx.x >= from && (int)blockIdx.x < from + n) {
+            found[0] = r0;
+            found[1] = from;
+            found[2] = n;
+            found[3] = mine;
         }
         __syncthreads();
-        if (lane == 31) scan[warp] = upto;
-        if (tid == 0) scan[kWarps] = -1;
-        __syncthreads();
-        for (int i = 0; i < warp; ++i) upto += (int)scan[i];
-        if (blockIdx.x < upto && blockIdx.x >= upto - n) {
-            scan[kWarps + 1] = upto - n;
-            scan[kWarps + 2] = n;
-            scan[kWarps + 3] = mine;
-            scan[kWarps] = r0;
-        }
-        __syncthreads();
-        if (scan[kWarps] < 0) return;
-        seg.row = (int)scan[kWarps];
-        first_team = (int)scan[kWarps + 1];
-        row_teams = (int)scan[kWarps + 2];
-        seg.row_n = (int)scan[kWarps + 3];
+        seg.row = found[0];
+        first_team = found[1];
+        row_teams = found[2];
+        seg.row_n = found[3];
         const int q = seg.row_n / row_teams, rem = seg.row_n - q * row_teams, j = blockIdx.x - first_team;
         seg.t0 = j * q + min(j, rem);
         seg.n = total = q + (j < rem);
     } else {
         // Teams that work: a tile at least for each warp where there are that few, but a team for each
         // row where that is more.
-        const long long room = (long long)gridDim.x * (kWarps / tn);
-        const long long wanted = max((all_tiles + tn - 1) / tn, min((long long)a.rows, all_tiles));
-        const unsigned teams = (unsigned)max(1LL, min(room, wanted));
-        share = all_tiles >> 32 ? all_tiles / teams : (unsigned)all_tiles / teams;
+        const int room = gridDim.x * (kWarps / tn);
+        const int teams = max(1, min(room, max((all_tiles + tn - 1) / tn, min(a.rows, all_tiles))));
+        share = all_tiles / teams;
         extra = all_tiles - share * teams;
-        const long long begin = team * share + min((long long)team, extra), end = begin + share + (team < extra);
-        // the thread that holds a team's first tile's row finds it
+        const int begin = team * share + min(team, extra);
+        total = share + (team < extra);
+        // each warp looks for the thread whose rows hold its team's first tile
+        int* starts = reinterpret_cast<int*>(smem + S::kState);  // not in use yet
+        starts[tid] = before;
         __syncthreads();
-        if (me == 0) scan[tn == 1 ? warp : 0] = team < teams && begin < end ? begin : -1;
-        __syncthreads();
-        for (int i = 0; i < kWarps / tn; ++i) {
-            const long long b = scan[i];
-            if (before <= b && b < before + mine) {
-                long long at = before;
-                int r = r0;
-                for (int n; at + (n = __ldcg(ws.tiles + r)) <= b; ++r) at += n;
-                scan[kWarps + 2 * i] = r;
-                scan[kWarps + 2 * i + 1] = at;
-            }
-        }
-        __syncthreads();
-        if (team >= teams || begin >= end) return;
-        total = (int)(end - begin);
-        seg.row = (int)scan[kWarps + (tn == 1 ? 2 * warp : 0)];
-        row_start = scan[kWarps + (tn == 1 ? 2 * warp + 1 : 1)];
-        seg.t0 = (int)(begin - row_start);
-        seg.row_n = __ldcg(ws.tiles + seg.row);
+        int below = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) below += starts[i * 32 + lane] <= begin;
+        const int holder = __reduce_add_sync(0xffffffffu, below) - 1;
+        row_start = starts[holder];
+        __syncthreads();  // the state's memory is given back
+        if (team >= teams || total == 0) return;
+        seg.row = holder * per_thread;
+        while (row_start + ws.tiles[seg.row] <= begin) row_start += ws.tiles[seg.row++];
+        seg.t0 = begin - row_start;
+        seg.row_n = ws.tiles[seg.row];
         seg.n = min(seg.row_n - seg.t0, total);
     }
 
@@ -767,28 +766,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
             c0 = first_team;
             c1 = first_team + row_teams - 1;
         } else if (!whole) {
-            auto holder = [&](long long tile) {
-                const long long longer = extra * (share + 1);
-                return (int)(tile < longer ? tile / (share + 1) : extra + (tile - longer) / share);
+            auto holder = [&](int tile) {
+                const int longer = extra * (share + 1);
+                return tile < longer ? tile / (share + 1) : extra + (tile - longer) / share;
             };
             c0 = holder(row_start);
             c1 = holder(row_start + seg.row_n - 1);
-            skew = row_start > c0 * share + min((long long)c0, extra);
+            skew = row_start > c0 * share + min(c0, extra);
         }
-        // four channels' sum of parts k0, k0 + step, ...
-        auto gather = [&](int h, int e, int k0, int step, float& m, float& l, float4& acc) {
-            m = -INFINITY, l = 0.f, acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int k = k0; k <= c1; k += step) {
-                const size_t at = (size_t)(2 * k + (k == c0 ? skew : 0)) * a.row_heads + h;
-                const float2 x = __ldcg(ws.part_ml + at);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(ws.part_o + at * D) + e);
-                const float n = fmaxf(m, x.x), ref = n == -INFINITY ? 0.f : n;
-                const float f = ptx::ex2(m - ref), f2 = ptx::ex2(x.x - ref);
-                m = n;
-                l = l * f + x.y * f2;
-                acc = make_float4(acc.x * f + v.x * f2, acc.y * f + v.y * f2, acc.z * f + v.z * f2, acc.w * f + v.w * f2);
-            }
+        // adds a part to a sum of four channels
+        auto join = [&](float& m, float& l, float4& acc, const float2& x, const float4& v) {
+            const float n = fmaxf(m, x.x), ref = n == -INFINITY ? 0.f : n;
+            const float f = ptx::ex2(m - ref), f2 = ptx::ex2(x.x - ref);
+            m = n;
+            l = l * f + x.y * f2;
+            acc = make_float4(acc.x * f + v.x * f2, acc.y * f + v.y * f2, acc.z * f + v.z * f2, acc.w * f + v.w * f2);
         };
         auto write = [&](int h, int e, float m, float l, const float4& acc) {
             const float f = l == 0.f ? 0.f : c.v_unit / l;
@@ -823,13 +815,30 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
                 if (lane == 0) last = atomicAdd(ws.done + seg.row, 1) == c1 - c0;
                 if (__shfl_sync(0xffffffffu, last, 0)) {
                     __threadfence();
-                    for (int i = lane; i < w.nh * (D / 4); i += 32) {
-                        const int h = i / (D / 4), e = i - h * (D / 4);
-                        float m, l;
-                        float4 acc;
-                        gather(h, e, c0, 1, m, l, acc);
-                        write(h, e, m, l, acc);
+                    // a lane has one float4 of each head (two heads for each half warp where D = 64): the
+                    // loads of all heads of two parts are in flight at once
+                    constexpr int kLanes = D / 4, kPer = 32 / kLanes, kSets = kRowHeads / kPer;
+                    const int e = lane % kLanes, hl = lane / kLanes;
+                    float m[kSets], l[kSets];
+                    float4 acc[kSets];
+#pragma unroll
+                    for (int i = 0; i < kSets; ++i) {
+                        m[i] = -INFINITY;
+                        l[i] = 0.f;
+                        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                     }
+#pragma unroll 2
+                    for (int k = c0; k <= c1; ++k) {
+                        const size_t at = (size_t)(2 * k + (k == c0 ? skew : 0)) * a.row_heads + hl;
+#pragma unroll
+                        for (int i = 0; i < kSets; ++i)
+                            if (i * kPer + hl < w.nh)
+                                join(m[i], l[i], acc[i], __ldcg(ws.part_ml + at + i * kPer),
+                                     __ldcg(reinterpret_cast<const float4*>(ws.part_o + (at + i * kPer) * D) + e));
+                    }
+#pragma unroll
+                    for (int i = 0; i < kSets; ++i)
+                        if (i * kPer + hl < w.nh) write(i * kPer + hl, e, m[i], l[i], acc[i]);
                 }
             }
         } else {
@@ -886,9 +895,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
                     const int quads = w.nh * (D / 4), groups = min(kWarps, max(1, kWarps * 32 / quads));
                     for (int i = tid; i < groups * quads; i += kWarps * 32) {
                         const int group = i / quads, x = i - group * quads, h = x / (D / 4), e = x - h * (D / 4);
-                        float m, l;
-                        float4 acc;
-                        gather(h, e, c0 + group, groups, m, l, acc);
+                        float m = -INFINITY, l = 0.f;
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                        for (int k = c0 + group; k <= c1; k += groups) {
+                            const size_t at = (size_t)(2 * k + (k == c0 ? skew : 0)) * a.row_heads + h;
+                            join(m, l, acc, __ldcg(ws.part_ml + at), __ldcg(reinterpret_cast<const float4*>(ws.part_o + at * D) + e));
+                        }
                         *reinterpret_cast<float4*>(state + (group * a.row_heads + h) * D + 4 * e) = acc;
                         if (e == 0) ml[group * kRowHeads + h] = make_float2(m, l);
                     }

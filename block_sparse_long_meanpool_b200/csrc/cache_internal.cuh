@@ -143,10 +143,7 @@ struct DecodeArgs {
 // The attention kernel has one CTA of kAttnWarps warps per multiprocessor, kMinCtas to kMaxCtas of
 // them; a team is a CTA, or a warp where there are more rows than CTAs, and leaves at most two parts
 // of rows to be merged.
-#ifndef CFG_WARPS
-#define CFG_WARPS 12
-#endif
-constexpr int kMinCtas = 128, kMaxCtas = 160, kAttnWarps = CFG_WARPS;
+constexpr int kMinCtas = 128, kMaxCtas = 160, kAttnWarps = 12;
 inline size_t most_parts(int rows) { return 2 * (size_t)kMaxCtas * (rows > kMinCtas ? kAttnWarps : 1); }
 struct DecodeWs {
     int2* items;     // [rows, max_items]: (page, heads that attend to it), ascending blocks

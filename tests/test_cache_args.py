@@ -119,6 +119,13 @@ def test_bad_arguments_are_refused(lib):
     assert lib.moba_cache_compact(r, None, FAKE, n, None) == I
 
 
+def test_decode_refuses_more_tiles_than_32_bits_count(lib):
+    wide = ctypes.byref(desc(num_seqs=1024, max_blocks=1 << 23))
+    assert lib.moba_cache_decode(wide, FAKE, 4, 3, 0.0, FAKE, 1 << 40, FAKE, FAKE, None) == moba.ERR_UNSUPPORTED
+    assert lib.moba_cache_decode_workspace_size(wide, 4, 3) == 0
+    assert lib.moba_cache_decode_workspace_size(ctypes.byref(desc(num_seqs=1024, max_blocks=1 << 18)), 4, 3) > 0
+
+
 def test_empty_calls_do_nothing(lib):
     r = ctypes.byref(desc())
     assert lib.moba_cache_append(r, None, None, None, None, 0, None, None, None) == moba.OK
