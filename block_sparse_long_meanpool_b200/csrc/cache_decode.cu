@@ -311,19 +311,16 @@ struct Tile {
     static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / kGroup;
     static constexpr int kK = 0, kV = kCodes, kKs = 2 * kCodes, kVs = kKs + kScales, kBytes = kVs + kScales;
 };
-// Shared memory: flags and the scan, the warps' state of a segment, and each warp's ring of tiles
-// with their barriers and what they hold (tokens, heads).  The state holds a row's heads only, so
-// that layers with few query heads per KV head may get longer rings.
+// Shared memory: flags and the scan, the warps' state of a segment (of a row's heads only, and only
+// where teams are CTAs), and the warps' rings of tiles with their barriers and what they hold (tokens,
+// heads).  The tiles that are left over go to the first warps, one each.
 template <int D>
 struct Smem {
     static constexpr int kMisc = 0;  // abort flag, last flag, scan
     static constexpr int kMl = 8 + 8 * kWarps + 16;   // [warps][heads] float2
     static constexpr int kState = (kMl + kWarps * kRowHeads * 8 + 127) / 128 * 128;  // [warps][row heads][D] fp32
-    __host__ __device__ static int ring(int heads) { return kState + kWarps * heads * D * 4; }
-    __host__ __device__ static int depth(int heads) {  // tiles of a warp's ring
-        const int n = (kSmem - ring(heads)) / (kWarps * (Tile<D>::kBytes + 16));
-        return n < kDepth ? n : kDepth;
-    }
+    static constexpr int kEntry = Tile<D>::kBytes + 16;  // a tile, its barrier and its meta
+    static_assert(kState + kWarps * kRowHeads * D * 4 + kWarps * kEntry <= kSmem, "a tile for each warp at least");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -408,9 +405,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
     const uint32_t base = ptx::smem_u32(smem);
     volatile int* abort_flag = reinterpret_cast<int*>(smem + S::kMisc);
     int* scan = reinterpret_cast<int*>(smem + S::kMisc + 8);
-    const int depth = S::depth(a.row_heads);  // the warp's ring, its barriers and metas
-    const int ring = S::ring(a.row_heads) + warp * depth * T::kBytes;
-    const int bars = S::ring(a.row_heads) + kWarps * depth * T::kBytes + warp * depth * 16, metas = bars + 8 * depth;
+    // the warp's ring, its barriers and metas
+    const int rings = S::kState + (a.rows > gridDim.x ? 0 : kWarps * a.row_heads * D * 4);
+    const int tiles = min((kSmem - rings) / S::kEntry, kWarps * kDepth), spread = tiles % kWarps;
+    const int depth = tiles / kWarps + (warp < spread), mine0 = warp * (tiles / kWarps) + min(warp, spread);
+    const int ring = rings + mine0 * T::kBytes;
+    const int bars = rings + tiles * T::kBytes + 16 * mine0, metas = bars + 8 * depth;
     if (lane < depth) {
         ptx::mbar_init(base + bars + 8 * lane, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
         for (int i = 0; i < kWarps; ++i) below += starts[i * 32 + lane] <= begin;
         const int holder = __reduce_add_sync(0xffffffffu, below) - 1;
         row_start = starts[holder];
-        __syncthreads();  // the state's memory is given back
+        ptx::fence_proxy_async();  // before the copies into these bytes
+        __syncthreads();
         if (team >= teams || total == 0) return;
         seg.row = holder * per_thread;
         while (row_start + ws.tiles[seg.row] <= begin) row_start += ws.tiles[seg.row++];
