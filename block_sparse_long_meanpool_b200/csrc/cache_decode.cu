@@ -358,6 +358,27 @@ __device__ __forceinline__ void lds(uint32_t (&w)[N], const unsigned char* at) {
     }
 }
 
+// Groups (bits) whose scale is a NaN for one of the tile's n tokens; those scales become 0.  One warp.
+template <int D>
+__device__ __forceinline__ uint32_t take_out_nans(unsigned char* scales, int n) {
+    constexpr int kPerTok = D / kGroup, kWords = kPerTok / 4;  // words of a token's scales
+    uint32_t* words = reinterpret_cast<uint32_t*>(scales);
+    uint32_t found = 0;
+    for (int i = threadIdx.x & 31; i < n * kWords; i += 32)
+        if (((words[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) found = 1;
+    if (!__any_sync(0xffffffffu, found)) return 0;
+    found = 0;
+    for (int i = threadIdx.x & 31; i < n * kWords; i += 32) {
+        const uint32_t nan = ((words[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // 0x80 in a NaN's byte
+        words[i] &= ~(nan | (nan - (nan >> 7)));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) found |= (nan >> (8 * b + 7) & 1) << (i % kWords * 4 + b);
+    }
+    ptx::fence_proxy_async();  // before a later copy into these bytes
+    __syncwarp();
+    return __reduce_or_sync(0xffffffffu, found);
+}
+
 // A team is a CTA's warps or, where rows are short, one warp.  Its tiles are [begin, end) of all
 // rows' tiles in order, warp i of the team taking every i-th; a segment is the part of a row in it.
 struct Segment {
@@ -539,7 +560,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
         const bool ok = (unsigned)item.x < (unsigned)c.pages;
         if (lane == 0) {
             *reinterpret_cast<int2*>(smem + metas + 8 * next_slot) =
-                make_int2(ok ? valid : 0, item.y | (valid < kTile || item.y != all_heads) << 8);
+                make_int2(ok ? valid : 0, item.y | (item.y != all_heads) << 8);
             if (ok) ptx::mbar_arrive_tx(bar, T::kBytes);
         }
         __syncwarp();
@@ -646,15 +667,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
                             mma16816(s[mt], lo[2], hi[2], lo[3], hi[3], qf[4 * i + 2], qf[4 * i + 3]);
                         }
                     }
-                    if (meta.y >> 8) {  // tokens behind the last one, heads that did not choose the block
-                        const bool on0 = meta.y >> (2 * t4) & 1, on1 = meta.y >> (2 * t4 + 1) & 1;
+                    const bool some = meta.y >> 8;  // not every head chose the block
+                    const bool off0 = some && !(meta.y >> (2 * t4) & 1), off1 = some && !(meta.y >> (2 * t4 + 1) & 1);
+                    if (ntok < kTile) {  // tokens behind the last one
 #pragma unroll
                         for (int mt = 0; mt < kTile / 16; ++mt)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const bool ok = mt * 16 + 8 * h + kr < ntok;
-                                s[mt][2 * h] = ok && on0 ? s[mt][2 * h] : -INFINITY;
-                                s[mt][2 * h + 1] = ok && on1 ? s[mt][2 * h + 1] : -INFINITY;
+                                s[mt][2 * h] = ok ? s[mt][2 * h] : -INFINITY;
+                                s[mt][2 * h + 1] = ok ? s[mt][2 * h + 1] : -INFINITY;
                             }
                     }
                     float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
@@ -663,6 +685,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
                         x0 = ptx::fmax3(x0, s[mt][0], s[mt][2]);
                         x1 = ptx::fmax3(x1, s[mt][1], s[mt][3]);
                     }
+                    x0 = off0 ? -INFINITY : x0;
+                    x1 = off1 ? -INFINITY : x1;
                     // The reference of the exponentials follows the maximum only when a score passes it by
                     // 2^kLag: p <= 2^kLag stays in fp16's range, and most tiles need no reduction over the
                     // warp and no rescaling.
@@ -689,16 +713,29 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
                     }
                     const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
                     uint32_t p[kTile / 16][2];
+                    float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
                     for (int mt = 0; mt < kTile / 16; ++mt)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float p0 = ptx::ex2(fmaf(s[mt][2 * h], unit0, -ref0));
                             const float p1 = ptx::ex2(fmaf(s[mt][2 * h + 1], unit1, -ref1));
-                            l0 += p0;
-                            l1 += p1;
+                            sum0 += p0;
+                            sum1 += p1;
                             p[mt][h] = transpose8x8(pack_f16(p0, p1));
                         }
+                    l0 += off0 ? 0.f : sum0;
+                    l1 += off1 ? 0.f : sum1;
+                    uint32_t nans = 0;  // scale groups of the values that hold a NaN
+                    if (some) {
+                        // p is 0 for the heads that did not choose the block (a thread's p is head g8's by now).
+                        // 0 times a NaN value would reach them all the same: such scales are taken out, and
+                        // their channels set for the heads that did choose it, below.
+                        if (!(meta.y >> g8 & 1))
+#pragma unroll
+                            for (int mt = 0; mt < kTile / 16; ++mt) p[mt][0] = p[mt][1] = 0;
+                        nans = take_out_nans<D>(src + T::kVs, ntok);
+                    }
                     if (ntok < kTile) {  // what lies behind the last token may be anything: scale 0
                         uint16_t* tail = reinterpret_cast<uint16_t*>(src + T::kVs);
                         for (int i = ntok * (D / kGroup / 2) + lane; i < kTile * (D / kGroup / 2); i += 32) tail[i] = 0;
@@ -736,6 +773,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 mma16816(o[4 * i + j], e[0][j], f[0][j], e[1][j], f[1][j], p[mt][0], p[mt][1]);
+                        }
+                    }
+                    if (nans >> (D == 128 ? g8 : g8 >> 1) & 1) {
+#pragma unroll
+                        for (int i = 0; i < kMt; ++i) {
+                            if (!off0) o[i][0] = o[i][2] = __int_as_float(0x7fffffff);
+                            if (!off1) o[i][1] = o[i][3] = __int_as_float(0x7fffffff);
                         }
                     }
                 }

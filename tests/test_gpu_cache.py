@@ -421,6 +421,38 @@ def test_decode_ranks_nan_scores_last_and_keeps_other_rows():
     assert abs(host(l)[0, 0] - (z.max() + np.log(np.exp(z - z.max()).sum()))) < 1e-4
 
 
+@pytest.mark.parametrize("d,heads", [(64, 1), (128, 2)])
+def test_nan_in_a_block_reaches_the_heads_that_chose_it_only(d, heads):
+    """A NaN scale of one token's values makes that group of channels NaN for the heads that attend to it, and
+    nothing else; one of its keys makes their whole output NaN.  The other heads' bits stay."""
+    rng = np.random.default_rng(26)
+    group = 4
+    c, m = pair(20, 1, 12, heads, d, 128)
+    fill(c, m, rng, [1300])
+    q = bf16(rng.standard_normal((1, heads * group, d))).cuda()
+    good_o, good_l = cache_decode(c, q, 3)
+    own = 1299 // 128
+    for kind, scales in (("v", c.v_scales), ("k", c.k_scales)):
+        for block in (2, 5, own):
+            page, grp = int(m.table[0, block]), d // 16 - 1
+            raw = scales.view(torch.uint8)
+            old = int(raw[page, 0, 7, grp])
+            raw[page, 0, 7, grp] = 0x7f
+            o, l = cache_decode(c, q, 3)
+            raw[page, 0, 7, grp] = old
+            for h in range(heads * group):
+                s = m.mean[m.table[0, :own], h // group] @ host(q)[0, h]
+                chose = h < group and (block == own or block in np.argsort(-s)[:2])
+                if not chose:
+                    assert torch.equal(o[0, h], good_o[0, h]) and torch.equal(l[h], good_l[h]), (kind, block, h)
+                elif kind == "v":
+                    assert torch.isnan(o[0, h, 16 * grp:16 * grp + 16]).all()
+                    assert torch.equal(o[0, h, :16 * grp], good_o[0, h, :16 * grp]) and torch.equal(l[h], good_l[h])
+                else:
+                    assert torch.isnan(o[0, h]).all() and torch.isnan(l[h]).all()
+    cache_status(c)
+
+
 def test_decode_reports_bad_pages_and_lengths():
     """A page out of range counts as no tokens, a length out of range as an empty slot; both are reported and
     the other sequences' results stay."""
