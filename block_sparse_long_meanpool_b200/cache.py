@@ -5,8 +5,9 @@ in pages of one block (``chunk_size`` tokens, every KV head) each, as e2m1 codes
 scale per 16 channels.  The calls append to it, attend over it and share, free and pack its
 pages; all of them are queued on the current stream of the cache's device and read lengths,
 tables and page counts there, so a serving loop never waits for the host and can be captured into
-a CUDA graph.  What the device finds wrong (no free page left, an index out of range) is kept in
-the cache's status word until ``cache_status`` reads it.
+a CUDA graph.  Each call takes its workspace from PyTorch's allocator unless it is given one; calls
+that may overlap, two graphs among them, must not share one.  What the device finds wrong (no free
+page left, an index out of range) is kept in the cache's status word until ``cache_status`` reads it.
 
     c = KVCache(num_pages=2048, num_seqs=64, max_blocks=64, num_kv_heads=8, head_dim=128, chunk_size=512)
     cache_reserve(c, upto)                        # pages for positions below upto[i]
@@ -162,6 +163,8 @@ def cache_append(c, k, v, cu_new, start, return_held=False):
     v, bf16 [n, Hkv, d], to the positions of sequence i from start[i] on (cu_new int32 [num_seqs + 1],
     start int32 [num_seqs]).  With ``return_held``, returns (k_held, v_held), bf16 like k and v: the
     values as the cache holds them, for the attention of the prompt itself."""
+    if k.dim() != 3:
+        _fail(f"k must be [new tokens, Hkv, d], got {tuple(k.shape)}")
     n = k.shape[0]
     shape = (n, c.num_kv_heads, c.head_dim)
     _need(k, "k", shape, torch.bfloat16, c.device)

@@ -227,6 +227,9 @@ moba_status moba_cache_decode(const moba_cache* c, const void* q, int num_q_head
     s = check_workspace(workspace, workspace_bytes, L.total);
     if (s != MOBA_OK) return s;
     const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)c->head_dim);
+    const float scale_log2 = ldexpf(scale * 1.4426950408889634f, c->k_exp);
+    if (std::isinf(scale_log2))
+        return fail(MOBA_ERR_INVALID_ARG, "softmax_scale %g with k_exp %d passes the range of fp32", softmax_scale, c->k_exp);
     cache::DecodeArgs a;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.hq = num_q_heads;
@@ -236,7 +239,7 @@ moba_status moba_cache_decode(const moba_cache* c, const void* q, int num_q_head
     a.rows = L.rows;
     a.row_heads = L.row_heads;
     a.max_items = L.max_items;
-    a.scale_log2 = ldexpf(scale * 1.4426950408889634f, c->k_exp);
+    a.scale_log2 = scale_log2;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
     cache::DecodeWs ws;

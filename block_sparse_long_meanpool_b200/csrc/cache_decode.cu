@@ -448,7 +448,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
     const int before = scan_threads(mine, scan, all_tiles);
 
     // Where there are more rows than CTAs, a team is one warp, and no warp waits for its CTA at a
-    // row's end; with fewer rows a row has so many parts that CTAs have to merge their own first.
+    // row's end (512 rows of about 69 tiles: 99 us, 112 us by CTAs); with fewer rows a row has so many
+    // parts that CTAs have to merge their own first (one row of 16K tiles would have 1776).
     const int tn = a.rows > gridDim.x ? 1 : kWarps;
     const int tw = tn == 1 ? 0 : warp, team = tn == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
     Segment seg;
@@ -459,7 +460,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
     int first_team = -1, row_teams = 0;  // where every team keeps to one row: the row's teams
     // A CTA that passes from one row to the next merges and starts twice, which costs about nine
     // tiles' time.  Where that is more than what keeping to one row costs (a row's CTAs are a whole
-    // number, so the fullest has up to rows / (CTAs - rows) more tiles than the average), it does.
+    // number, so the fullest has up to rows / (CTAs - rows) more tiles than the average), it does: 8
+    // rows of 128 tiles take 13 us, 17 us where CTAs pass from row to row.
     const int spare = (int)gridDim.x - a.rows;
     int* found = scan + 2 * kWarps;  // what the thread that holds a row tells the CTA
     if (spare > 0 && (long long)all_tiles * a.rows < 9LL * gridDim.x * spare) {
@@ -980,8 +982,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cache_attn_kernel(View c, Deco
 template <int D, int K>
 cudaError_t launch_plan(const View& c, const DecodeArgs& a, const DecodeWs& ws, int num_sms, cudaStream_t st) {
     // A CTA scores 64 blocks at a time.  Where a row may have more than two such rounds and the rows
-    // are too few to fill the GPU, eight CTAs share one.
-    const int cs = a.topk > 1 && c.max_blocks > 128 && a.rows * 2 <= num_sms ? 8 : 1;
+    // are too few to fill the GPU, a cluster shares one.  The whole step, with clusters of 1, 4 and 8:
+    // 8 rows of 2048 blocks 75, 34, 27 us; 32 rows of 512 blocks 32, 22.5, 21 us; 64 rows of 256 blocks
+    // 33.5, 30, 34 us; 64 rows of 128 blocks 29.5, 29, 33 us; 4 rows of 8 blocks 10.1, 11.2, 11.1 us.
+    const int cs = a.topk <= 1 || c.max_blocks <= 128 ? 1 : a.rows * 4 <= num_sms ? 8 : a.rows * 2 <= num_sms ? 4 : 1;
     if (cs == 1) {
         cache_plan_kernel<D, K><<<a.rows, kThreads, 0, st>>>(c, a, ws);
         return cudaGetLastError();

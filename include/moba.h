@@ -281,8 +281,10 @@ moba_status moba_decode_minmax_fwd(const moba_params* p, const void* q, const vo
  * 16-byte aligned.  The int32 contents are read on the device: an index out of range, a shared
  * page that would be written or a length that does not fit is reported in `status`, and the
  * sequence (or, where a call says so, the whole call) is left out; nothing out of bounds is
- * accessed.  Calls on one cache are ordered by their stream; calls on several streams that
- * touch the same cache are the caller's to order.
+ * accessed.  Calls on one cache are ordered by their stream; calls on several streams are the
+ * caller's to order where one of them writes the cache, and calls that may overlap need workspaces
+ * of their own (a graph keeps the workspace that it was captured with).  The stream belongs to the
+ * current device, as the buffers do.
  *   Limits: head_dim 64 or 128, chunk_size a multiple of 128, num_seqs <= 65535,
  *   max_blocks * chunk_size < 2^31, |k_exp|, |v_exp| <= 64 (MOBA_ERR_UNSUPPORTED). */
 typedef struct {

@@ -107,8 +107,10 @@ def test_bad_arguments_are_refused(lib):
     for hq, topk, want in ((3, 3, I), (0, 3, I), (-2, 3, I), (4, -1, I), (4, 33, U)):
         assert lib.moba_cache_decode(r, FAKE, hq, topk, 0.0, FAKE, n, FAKE, FAKE, None) == want
         assert lib.moba_cache_decode_workspace_size(r, hq, topk) == 0
-    for scale in (float("nan"), float("inf")):
+    for scale in (float("nan"), float("inf"), 3e38):
         assert lib.moba_cache_decode(r, FAKE, 4, 3, scale, FAKE, n, FAKE, FAKE, None) == I
+    wide = ctypes.byref(desc(k_exp=64))
+    assert lib.moba_cache_decode(wide, FAKE, 4, 3, 1e30, FAKE, n, FAKE, FAKE, None) == I
     assert lib.moba_cache_decode(r, FAKE + 8, 4, 3, 0.0, FAKE, n, FAKE, FAKE, None) == I
     # compact: another geometry, a shared buffer
     other = dict(k_codes=2 * FAKE, k_scales=2 * FAKE, v_codes=2 * FAKE, v_scales=2 * FAKE, k_mean=2 * FAKE,

@@ -708,6 +708,34 @@ def test_a_serving_run():
         same(c, m)
 
 
+@pytest.mark.parametrize("topk", [1, 3, 32])
+def test_the_package_s_other_paths_agree(topk):
+    """The prompt's forward over the held values, the packed decode step over them, and the decode step over the
+    cache: the same attention three ways, at the last token of each sequence.  The packed paths round p and
+    their partial results to bf16, so their own tolerances (2e-2, lse 1e-3) apply."""
+    rng = np.random.default_rng(44)
+    heads, group, d, chunk, lens = 2, 4, 128, 128, [1300, 513, 128]
+    n, cu = sum(lens), np.concatenate([[0], np.cumsum(lens)])
+    k, v = (bf16(rng.standard_normal((n, heads, d))).cuda() for _ in "kv")
+    k += 0.5 * bf16(rng.standard_normal((n // 64 + 1, heads, d))).cuda().repeat_interleave(64, 0)[:n]
+    q = bf16(rng.standard_normal((n, heads * group, d))).cuda()
+    c = KVCache(24, 3, 12, heads, d, chunk)
+    cache_reserve(c, ints(lens))
+    hk, hv = cache_append(c, k, v, ints(cu), ints([0, 0, 0]), return_held=True)
+    last = torch.tensor(cu[1:] - 1).cuda()
+    o, l = cache_decode(c, q[last], topk)
+    cache_status(c)
+    po, pl, sel = moba.attn_fwd(q, hk, hv, ints(cu), chunk, topk, return_sel=True)
+    means = moba.meanpool(hk, ints(cu), chunk)
+    do, dl = moba.decode_fwd(q[last], hk, hv, ints(cu), means, chunk, topk)
+    assert (o.float() - po[last].float()).abs().max() <= 2e-2 and (l - pl[:, last]).abs().max() <= 1e-3
+    assert (o.float() - do.float()).abs().max() <= 2e-2 and (l - dl).abs().max() <= 1e-3
+    # a block's k_mean is what the packed path pools
+    blocks = [moba.num_blocks(lens[:i], chunk) + j for i in range(3) for j in range(lens[i] // chunk)]
+    pages = [int(c.table[i, j]) for i in range(3) for j in range(lens[i] // chunk)]
+    assert torch.allclose(c.k_mean[pages], means[blocks], rtol=0, atol=2.0 ** -20)
+
+
 def test_a_captured_step_replays():
     """Reserve, append and decode of one token captured into a graph, replayed with other inputs, equal the
     eager calls; two graphs with workspaces of their own run on two streams at once."""
