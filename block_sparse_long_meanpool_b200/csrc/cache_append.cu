@@ -25,18 +25,20 @@ constexpr int kSeg = 64;  // positions per segment, aligned within a block (chun
 
 // The idx-th unit of `unit` positions that new tokens touch, over all sequences (whole == false),
 // or the idx-th unit that they complete (whole == true).  Called by one warp; every lane gets the
-// sequence (-1 past the last) and the unit's index within it.
+// sequence (-1 past the last) and the unit's index within it.  Sequences behind a fall of cu_new have
+// no units: the rest have rows of their own, so the launch's bounds on the units hold.
 __device__ __forceinline__ int find_unit(const View& c, const AppendArgs& a, int unit, bool whole,
                                          int idx, NewTokens& t, int& u) {
     const int lane = threadIdx.x & 31;
     int base = 0;
     for (int i0 = 0; i0 < c.seqs; i0 += 32) {
         const int i = i0 + lane;
-        NewTokens m{0, 0, 0};
+        NewTokens m{0, 0, 0, false};
         bool bad = false;
         if (i < c.seqs) m = new_tokens(c, a.cu, a.start, a.total, i, &bad);
         int n = 0;
-        if (m.n > 0)
+        const unsigned falls = __ballot_sync(0xffffffffu, m.falls);
+        if (m.n > 0 && (falls & ((1u << lane) - 1)) == 0)
             n = whole ? (m.first + m.n) / unit - m.first / unit
                       : (m.first + m.n - 1) / unit - m.first / unit + 1;
         int incl = n;
@@ -56,6 +58,7 @@ __device__ __forceinline__ int find_unit(const View& c, const AppendArgs& a, int
             u += t.first / unit;
             return i0 + src;
         }
+        if (falls) break;
         base += __shfl_sync(0xffffffffu, incl, 31);
     }
     return -1;
@@ -135,6 +138,7 @@ __device__ __forceinline__ void move_length(const View& c, const AppendArgs& a, 
     if (bad && lane == 0) report(c, MOBA_ERR_INVALID_ARG);
     if (t.n == 0) return;
     bool ok = true;
+    for (int j = lane; j < i; j += 32) ok = ok && __ldg(a.cu + j) <= __ldg(a.cu + j + 1);
     for (int j = t.first / c.chunk + lane; j <= (t.first + t.n - 1) / c.chunk; j += 32)
         ok = ok && own_page(c, __ldg(c.table + (size_t)i * c.max_blocks + j));
     ok = __all_sync(0xffffffffu, ok);

@@ -320,7 +320,8 @@ moba_status moba_cache_reserve(const moba_cache* c, const int* upto, void* works
  *   the group gives scale NaN and codes 0.  k_mean of a completed block is the mean of its held
  *   keys (fp32 sums), whichever calls wrote them.
  *   k, v            bf16 [new_tokens, Hkv, d] device
- *   cu_new          int32 [num_seqs + 1] device, start int32 [num_seqs] device
+ *   cu_new          int32 [num_seqs + 1] device, never falling (the sequences behind a fall are
+ *                   left out with the one at it), start int32 [num_seqs] device
  *   k_held, v_held  bf16 [new_tokens, Hkv, d] device or NULL: receive the values as held (for the
  *                   attention of the prompt itself) */
 moba_status moba_cache_append(const moba_cache* c, const void* k, const void* v, const int* cu_new,

@@ -251,6 +251,28 @@ def test_append_takes_tokens_back_and_refuses_gaps():
     cache_status(c)
 
 
+@pytest.mark.parametrize("rows,seqs,chunk", [(1, 3, 128), (300, 3, 512), (7, 70, 128), (300, 70, 512)])
+def test_append_leaves_out_what_is_behind_a_fall_of_cu_new(rows, seqs, chunk):
+    """Sequences behind a fall would name rows again, more in all than there are: no length covers tokens that
+    were not written."""
+    rng = np.random.default_rng(rows + seqs)
+    c, m = pair(2 * seqs, seqs, 2, 1, 64, chunk)
+    fill(c, m, rng, [5] * seqs)
+    cache_reserve(c, ints([5 + rows] * seqs))
+    cache_status(c)
+    m.reserve([5 + rows] * seqs)
+    k, v = (bf16(rng.standard_normal((rows, 1, 64))) for _ in "kv")
+    first = seqs // 2
+    cu = [0] * first + [rows] + [0, rows] * seqs  # a fall behind each sequence that names the rows
+    cu = cu[:seqs + 1]
+    m.append(k.double().numpy(), v.double().numpy(), cu[:first + 1] + [rows] * (seqs - first), [5] * seqs)
+    cache_append(c, k.cuda(), v.cuda(), ints(cu), ints([5] * seqs))
+    with pytest.raises(moba.MobaError) as e:
+        cache_status(c)
+    assert e.value.status == moba.ERR_INVALID_ARG
+    same(c, m)
+
+
 def test_append_needs_pages_of_its_own():
     """No page, a page out of range and a shared page are reported; the length stays."""
     rng = np.random.default_rng(13)
